@@ -438,6 +438,197 @@ kvtc_status kvtc_lossless_decode(kvtc_codec* codec, const kvtc_job* jobs, int32_
  * workspace to host memory; synchronises `stream` first. */
 kvtc_status kvtc_lossless_sizes(const void* d_ws, int32_t n_jobs, uint64_t* sizes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The paged cache in use. kvtc_decode restores K and V into pages
+ * ([n_blocks, block_size, F] rows behind a block table); the calls below
+ * keep such a cache running on the GPU: block tables and slot maps from
+ * request lengths, the write of new rows, attention of one new token per
+ * request over its pages, key bounds per page, and the selection of the
+ * pages worth attending.
+ *
+ * None of them needs a codec. They take their sizes from the host and every
+ * length, table and slot from device memory, allocate nothing, enqueue only
+ * on `stream` and never synchronise it, so they can be captured into a HIP
+ * graph and replayed on new contents. A workspace holds nothing between
+ * calls: it needs no clearing, and calls that follow each other on one
+ * stream may share it; calls that may overlap may not.
+ *
+ * Host errors (KVTC_E_INVALID, KVTC_E_CAPACITY, KVTC_E_UNSUPPORTED) enqueue
+ * nothing. What only the device can see sets status words: status, where it
+ * is not NULL, is int32 device memory that the caller zeroes; a request (for
+ * kvtc_page_write: the call) that had an error gets its negative kvtc_status
+ * there, one without leaves its word as it was.
+ *
+ * Pages of KVTC_BF16 or KVTC_F32; any block_size; head_dim a multiple of 8
+ * up to KVTC_MAX_HEAD_DIM; n_blocks * block_size < 2^31; at most
+ * KVTC_MAX_JOBS requests per call. Page, bounds, q and out pointers are
+ * 16-byte aligned, strides count elements and are multiples of 8.
+ * ---------------------------------------------------------------------- */
+
+/* Largest head_dim the paged calls take. */
+#define KVTC_MAX_HEAD_DIM 256
+
+/* The K and V pages of one layer: row block * block_size + offset of
+ * kv_heads * head_dim elements, heads concatenated, as kvtc_decode writes
+ * them. The capacities are the bytes available at k and v. */
+typedef struct {
+  void* k;
+  void* v;
+  size_t k_capacity;
+  size_t v_capacity;
+  int32_t n_blocks;
+  int32_t block_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;           /* kvtc_dtype of the pages                        */
+} kvtc_pages;
+
+/* The requests of a call. Token t of request i is row
+ * block_table[i * table_stride + t / block_size] * block_size + t % block_size.
+ * A request with lens[i] < 0 or > table_width * block_size counts as empty
+ * and gets status KVTC_E_INVALID. Table entries behind a request's last page
+ * are not read. An entry outside [0, n_blocks) leaves its tokens out and gives
+ * status KVTC_E_INVALID. */
+typedef struct {
+  const int32_t* block_table;  /* device [n_requests, table_stride]          */
+  const int32_t* lens;         /* device [n_requests]: tokens in the cache   */
+  int32_t* status;             /* device [n_requests], or NULL               */
+  int32_t n_requests;
+  int32_t table_width;         /* entries of a request's table row           */
+  int32_t table_stride;        /* elements between table rows, >= table_width */
+} kvtc_requests;
+
+/* Growth of the requests from old_lens to new_lens tokens. */
+typedef struct {
+  const int32_t* old_lens;     /* device [n_requests]; NULL: all 0           */
+  const int32_t* new_lens;     /* device [n_requests], >= old_lens           */
+  const int32_t* free_blocks;  /* device [n_free]: distinct unused pages     */
+  const int32_t* free_from;    /* device: first unused entry of free_blocks; NULL: 0 */
+  int32_t* block_table;        /* device [n_requests, table_stride], updated */
+  int32_t* slots;              /* device [n_slots], written                  */
+  int32_t* starts;             /* device [n_requests + 1], written, or NULL  */
+  int32_t* taken;              /* device: number of pages taken, or NULL     */
+  int32_t* status;             /* device [n_requests], or NULL               */
+  int32_t n_requests;
+  int32_t block_size;
+  int32_t n_blocks;            /* pages of the cache                         */
+  int32_t n_free;
+  int32_t table_width;
+  int32_t table_stride;
+  int32_t n_slots;
+} kvtc_page_plan;
+
+/* Block tables and slot maps for a step that appends new_lens[i] - old_lens[i]
+ * tokens to every request i. The request needs ceil(new / block_size) -
+ * ceil(old / block_size) more pages; they come from free_blocks in request
+ * order, from entry *free_from on, and go behind the request's pages in its
+ * table row (the row's other entries stay as they are). The new tokens of all
+ * requests are numbered through in request order: starts[i] is the first of
+ * request i and starts[n_requests] their number, and slots[starts[i] + j] is
+ * the row of token old_lens[i] + j (block_table entry * block_size + offset).
+ * slots behind the last token, up to n_slots, are -1.
+ *
+ * A request is refused, gets no pages, an unchanged table row and slots of
+ * -1, with a status of
+ *   KVTC_E_INVALID   if old < 0, new < old, new > table_width * block_size
+ *                    (it then counts as growing by no token), or
+ *   KVTC_E_CAPACITY  if its tokens end past n_slots, or it needs pages and
+ *                    *free_from plus those that the requests before it need,
+ *                    refused for want of pages or not, leave too few;
+ * a page outside [0, n_blocks), old or taken, gives its tokens the slot -1
+ * and the status KVTC_E_INVALID. *taken is the number of pages given out, so
+ * the caller's next free_from is *free_from + *taken. An *free_from < 0 is
+ * read as 0. The outputs may not overlap the inputs. Errors: KVTC_E_INVALID,
+ * and KVTC_E_UNSUPPORTED for a cache of 2^31 rows or more. */
+kvtc_status kvtc_page_tables(const kvtc_page_plan* plan, hipStream_t stream);
+
+/* New rows of K and V. */
+typedef struct {
+  const void* k;           /* device, row i at k + i * k_stride elements     */
+  const void* v;
+  const int32_t* slots;    /* device [n_rows]                                */
+  int32_t* status;         /* device, one word, or NULL                      */
+  int64_t k_stride;
+  int64_t v_stride;
+  int32_t n_rows;
+  int32_t dtype;           /* kvtc_dtype of the rows                         */
+} kvtc_page_rows;
+
+/* Write row i of rows->k and rows->v to row slots[i] of the pages, converted
+ * to the pages' type (round to nearest even) where it differs. A row with a
+ * slot below 0 is skipped; one with a slot past the pages too, with status
+ * KVTC_E_INVALID. Slots are distinct: of two rows with one slot, each element
+ * comes from either. The rows may be any element-aligned view (a slice of a
+ * fused projection, say); they go in 16-byte pieces where rows, strides and F
+ * allow. */
+kvtc_status kvtc_page_write(const kvtc_pages* pages, const kvtc_page_rows* rows, hipStream_t stream);
+
+/* Key bounds of the pages that hold tokens [from_lens[i], lens[i]) of request
+ * i (from_lens NULL: all its pages; a value below 0 is read as 0):
+ * bounds[page] = the smallest, then the largest value of each of the F
+ * features over the page's rows below lens[i], [n_blocks, 2, F] in the pages'
+ * type; bounds of other pages stay as they are. A NaN among the rows makes
+ * both NaN. bounds_capacity: bytes at bounds. pages->v may be NULL here. */
+kvtc_status kvtc_page_bounds(const kvtc_pages* pages, const kvtc_requests* requests,
+                             const int32_t* from_lens, void* bounds, size_t bounds_capacity,
+                             hipStream_t stream);
+
+/* One new token per request: q and out hold q_heads * head_dim elements of
+ * the pages' type per request, q_stride and out_stride elements apart (0: the
+ * rows follow each other). q_heads is a multiple of kv_heads; query head h
+ * reads KV head h / (q_heads / kv_heads). */
+typedef struct {
+  const void* q;           /* device                                         */
+  void* out;               /* device, written by kvtc_page_attend            */
+  float* lse;              /* device [n_requests, q_heads], or NULL          */
+  int64_t q_stride;
+  int64_t out_stride;
+  int32_t q_heads;
+  float scale;             /* of the products q.k, e.g. 1 / sqrt(head_dim)   */
+} kvtc_queries;
+
+/* Pages selected for every (request, KV head): up to `budget` indexes into the
+ * request's table row. */
+typedef struct {
+  int32_t* blocks;         /* device [n_requests, kv_heads, budget]          */
+  int32_t budget;          /* > 0                                            */
+  int32_t first;           /* kvtc_page_select keeps a request's first pages */
+  int32_t last;            /* and its last ones; first + last <= budget      */
+} kvtc_selection;
+
+/* Workspace bytes of kvtc_page_attend, and of kvtc_page_select where
+ * selection is not NULL (one workspace serves both in turn). 0 on arguments
+ * that these calls would refuse. Depends on sizes only. */
+size_t kvtc_page_workspace_bytes(const kvtc_pages* pages, const kvtc_requests* requests,
+                                 const kvtc_queries* queries, const kvtc_selection* selection);
+
+/* Select pages by a score on their key bounds. For request i and KV head h,
+ * with q the head's G = q_heads / kv_heads queries,
+ *   score_j = sum_d (sum_g max(q_gd, 0)) hi_jd + (sum_g min(q_gd, 0)) lo_jd,
+ * which no sum over g of one product q_g.k with a key of page j exceeds; it
+ * is summed in fp64 and rounded to fp32. The request's `first` first and
+ * `last` last pages are kept always, then those of the highest scores (a NaN
+ * counts as higher than any number), ties to the lower index, up to `budget`
+ * pages in all. blocks lists them in ascending order, then -1. The scale of
+ * the products (positive) plays no part. Table entries outside [0, n_blocks)
+ * are never selected. queries->out may be NULL here. */
+kvtc_status kvtc_page_select(const kvtc_pages* pages, const kvtc_requests* requests,
+                             const kvtc_queries* queries, const void* bounds, size_t bounds_capacity,
+                             const kvtc_selection* selection, void* d_ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* Attention of one new token: for every request and query head
+ *   out = sum_t softmax_t(scale q.k_t) v_t,  lse = log sum_t exp(scale q.k_t)
+ * over the tokens t < lens[i], or with a selection over those of them in the
+ * selected pages (entries below 0 or past the request's pages are left out; a
+ * page listed twice counts twice). No tokens: out = 0 and lse = -inf. Rows of
+ * a page behind lens[i] are never used, whatever they hold. Sums and the
+ * softmax's maximum and sum are fp32; out is rounded once. Equal calls give
+ * equal bits. */
+kvtc_status kvtc_page_attend(const kvtc_pages* pages, const kvtc_requests* requests,
+                             const kvtc_queries* queries, const kvtc_selection* selection,
+                             void* d_ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,7 @@ KVTC_F32, KVTC_BF16 = 0, 1
 KVTC_K, KVTC_V = 0, 1
 KVTC_MAX_REFF = 256
 KVTC_MAX_JOBS = 4096
+KVTC_MAX_HEAD_DIM = 256
 KVTC_CAL_SHARED_BASIS, KVTC_CAL_GLOBAL_BUDGET, KVTC_CAL_COMPONENT_WIDTHS = 1, 2, 4
 
 
@@ -47,6 +48,42 @@ class kvtc_slot_info(C.Structure):
     _fields_ = [("calibrated", C.c_int32), ("n_act", C.c_int32), ("r_eff", C.c_int32),
                 ("record_bytes", C.c_int32), ("slot_id", C.c_uint64),
                 ("widths", C.c_uint8 * 512), ("per_component", C.c_int32), ("folded_mean", C.c_int32)]
+
+
+class kvtc_pages(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_capacity", C.c_size_t),
+                ("v_capacity", C.c_size_t), ("n_blocks", C.c_int32), ("block_size", C.c_int32),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("dtype", C.c_int32)]
+
+
+class kvtc_requests(C.Structure):
+    _fields_ = [("block_table", C.c_void_p), ("lens", C.c_void_p), ("status", C.c_void_p),
+                ("n_requests", C.c_int32), ("table_width", C.c_int32), ("table_stride", C.c_int32)]
+
+
+class kvtc_page_plan(C.Structure):
+    _fields_ = [("old_lens", C.c_void_p), ("new_lens", C.c_void_p), ("free_blocks", C.c_void_p),
+                ("free_from", C.c_void_p), ("block_table", C.c_void_p), ("slots", C.c_void_p),
+                ("starts", C.c_void_p), ("taken", C.c_void_p), ("status", C.c_void_p),
+                ("n_requests", C.c_int32), ("block_size", C.c_int32), ("n_blocks", C.c_int32),
+                ("n_free", C.c_int32), ("table_width", C.c_int32), ("table_stride", C.c_int32),
+                ("n_slots", C.c_int32)]
+
+
+class kvtc_page_rows(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("slots", C.c_void_p), ("status", C.c_void_p),
+                ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("n_rows", C.c_int32),
+                ("dtype", C.c_int32)]
+
+
+class kvtc_queries(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("out", C.c_void_p), ("lse", C.c_void_p), ("q_stride", C.c_int64),
+                ("out_stride", C.c_int64), ("q_heads", C.c_int32), ("scale", C.c_float)]
+
+
+class kvtc_selection(C.Structure):
+    _fields_ = [("blocks", C.c_void_p), ("budget", C.c_int32), ("first", C.c_int32),
+                ("last", C.c_int32)]
 
 
 class KvtcError(RuntimeError):
@@ -97,6 +134,12 @@ def lib():
         "kvtc_lossless_encode": (st, [vp, vp, i32, vp, sz, vp]),
         "kvtc_lossless_decode": (st, [vp, vp, i32, vp, sz, vp]),
         "kvtc_lossless_sizes": (st, [vp, i32, C.POINTER(C.c_uint64), vp]),
+        "kvtc_page_tables": (st, [vp, vp]),
+        "kvtc_page_write": (st, [vp, vp, vp]),
+        "kvtc_page_bounds": (st, [vp, vp, vp, vp, sz, vp]),
+        "kvtc_page_workspace_bytes": (sz, [vp, vp, vp, vp]),
+        "kvtc_page_select": (st, [vp, vp, vp, vp, sz, vp, vp, sz, vp]),
+        "kvtc_page_attend": (st, [vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -144,6 +187,60 @@ def make_job(layer, kind, n_tokens, src, dst, dst_capacity, block_table=None, bl
         src_capacity = src.numel() * src.element_size()
     return kvtc_job(int(layer), int(kind), int(n_tokens), _ptr(src), int(src_capacity), _ptr(dst),
                     int(dst_capacity), _ptr(block_table), int(block_size), int(n_blocks))
+
+
+def _bytes(x, n, what) -> int:
+    """The capacity n, or the byte size of x when x is a tensor."""
+    if n is not None:
+        return int(n)
+    if x is None:
+        return 0
+    if not hasattr(x, "numel"):
+        raise ValueError(f"{what} is required when its buffer is a raw pointer")
+    return x.numel() * x.element_size()
+
+
+# The descriptors of the paged-cache calls. Buffers are tensors or pointers;
+# a descriptor holds their addresses only, so the caller keeps them alive.
+
+def make_pages(k, v, n_blocks, block_size, kv_heads, head_dim, dtype, k_capacity=None,
+               v_capacity=None) -> kvtc_pages:
+    """The capacities default to the byte sizes of k and v when they are tensors."""
+    return kvtc_pages(_ptr(k), _ptr(v), _bytes(k, k_capacity, "k_capacity"),
+                      _bytes(v, v_capacity, "v_capacity"), n_blocks, block_size, kv_heads, head_dim,
+                      dtype)
+
+
+def make_requests(block_table, table_width, lens, n_requests, status=None,
+                  table_stride=None) -> kvtc_requests:
+    """table_stride defaults to table_width."""
+    return kvtc_requests(_ptr(block_table), _ptr(lens), _ptr(status), n_requests, table_width,
+                         table_width if table_stride is None else table_stride)
+
+
+def make_page_plan(old_lens, new_lens, n_requests, block_size, free_blocks, n_free, n_blocks,
+                   block_table, table_width, slots, n_slots, free_from=None, starts=None, taken=None,
+                   status=None, table_stride=None) -> kvtc_page_plan:
+    """old_lens None: every request starts empty; table_stride defaults to table_width."""
+    return kvtc_page_plan(_ptr(old_lens), _ptr(new_lens), _ptr(free_blocks), _ptr(free_from),
+                          _ptr(block_table), _ptr(slots), _ptr(starts), _ptr(taken), _ptr(status),
+                          n_requests, block_size, n_blocks, n_free, table_width,
+                          table_width if table_stride is None else table_stride, n_slots)
+
+
+def make_page_rows(k, v, n_rows, slots, dtype, k_stride, v_stride, status=None) -> kvtc_page_rows:
+    """k_stride and v_stride: elements between rows (tensor.stride(0))."""
+    return kvtc_page_rows(_ptr(k), _ptr(v), _ptr(slots), _ptr(status), k_stride, v_stride, n_rows,
+                          dtype)
+
+
+def make_queries(q, out, q_heads, scale, lse=None, q_stride=0, out_stride=0) -> kvtc_queries:
+    """q_stride and out_stride: elements between requests, 0 for rows that follow each other."""
+    return kvtc_queries(_ptr(q), _ptr(out), _ptr(lse), q_stride, out_stride, q_heads, scale)
+
+
+def make_selection(blocks, budget, first=0, last=0) -> kvtc_selection:
+    return kvtc_selection(_ptr(blocks), budget, first, last)
 
 
 # ------------------------------------------------------------ C entry points ---
@@ -289,6 +386,46 @@ def kvtc_lossless_sizes(d_ws, n_jobs: int, stream=None) -> np.ndarray:
     _check(lib().kvtc_lossless_sizes(_ptr(d_ws), n_jobs, out.ctypes.data_as(C.POINTER(C.c_uint64)),
                                      _stream(stream)))
     return out
+
+
+def _ref(d):
+    return None if d is None else C.byref(d)
+
+
+def kvtc_page_tables(plan: kvtc_page_plan, stream=None) -> None:
+    _check(lib().kvtc_page_tables(_ref(plan), _stream(stream)))
+
+
+def kvtc_page_write(pages: kvtc_pages, rows: kvtc_page_rows, stream=None) -> None:
+    _check(lib().kvtc_page_write(_ref(pages), _ref(rows), _stream(stream)))
+
+
+def kvtc_page_bounds(pages: kvtc_pages, requests: kvtc_requests, from_lens, bounds,
+                     bounds_capacity=None, stream=None) -> None:
+    _check(lib().kvtc_page_bounds(_ref(pages), _ref(requests), _ptr(from_lens), _ptr(bounds),
+                                  _bytes(bounds, bounds_capacity, "bounds_capacity"),
+                                  _stream(stream)))
+
+
+def kvtc_page_workspace_bytes(pages: kvtc_pages, requests: kvtc_requests, queries: kvtc_queries,
+                              selection: kvtc_selection | None = None) -> int:
+    return lib().kvtc_page_workspace_bytes(_ref(pages), _ref(requests), _ref(queries),
+                                           _ref(selection))
+
+
+def kvtc_page_select(pages: kvtc_pages, requests: kvtc_requests, queries: kvtc_queries, bounds,
+                     selection: kvtc_selection, d_ws, ws_bytes=None, bounds_capacity=None,
+                     stream=None) -> None:
+    _check(lib().kvtc_page_select(_ref(pages), _ref(requests), _ref(queries), _ptr(bounds),
+                                  _bytes(bounds, bounds_capacity, "bounds_capacity"),
+                                  _ref(selection), _ptr(d_ws), _bytes(d_ws, ws_bytes, "ws_bytes"),
+                                  _stream(stream)))
+
+
+def kvtc_page_attend(pages: kvtc_pages, requests: kvtc_requests, queries: kvtc_queries,
+                     selection: kvtc_selection | None, d_ws, ws_bytes=None, stream=None) -> None:
+    _check(lib().kvtc_page_attend(_ref(pages), _ref(requests), _ref(queries), _ref(selection),
+                                  _ptr(d_ws), _bytes(d_ws, ws_bytes, "ws_bytes"), _stream(stream)))
 
 
 def kvtc_deflate(data: bytes, level: int = 6) -> bytes:

@@ -34,7 +34,10 @@ def _run(cmd, verbose):
 
 
 # gfx950 kernel translation units (compiled in parallel)
-HIP_SOURCES = ["kvtc_encode.hip", "kvtc_decode.hip", "kvtc_lossless.hip"]
+HIP_SOURCES = ["kvtc_encode.hip", "kvtc_decode.hip", "kvtc_lossless.hip", "kvtc_pages.hip"]
+
+# the host core: the codec, and the checks of the paged-cache calls
+HOST_SOURCES = ["kvtc_host.cpp", "kvtc_pages_host.cpp"]
 
 
 def build(verbose: bool = False) -> str:
@@ -44,9 +47,9 @@ def build(verbose: bool = False) -> str:
     for src in HIP_SOURCES:
         o = os.path.join(BUILD, src.replace(".hip", ".o"))
         steps.append((o, [HIPCC, *HIP_FLAGS, *inc, "-c", os.path.join(CSRC, src), "-o", o]))
-    o = os.path.join(BUILD, "kvtc_host.o")
-    steps.append((o, [HIPCC, "-O3", "-std=c++17", "-fPIC", *inc, "-c",
-                      os.path.join(CSRC, "kvtc_host.cpp"), "-o", o]))
+    for src in HOST_SOURCES:
+        o = os.path.join(BUILD, src.replace(".cpp", ".o"))
+        steps.append((o, [HIPCC, "-O3", "-std=c++17", "-fPIC", *inc, "-c", os.path.join(CSRC, src), "-o", o]))
     o = os.path.join(BUILD, "kvtc_linalg.o")
     steps.append((o, ["g++", "-O3", "-march=x86-64-v3", "-std=c++17", "-fPIC", *inc, "-c",
                       os.path.join(CSRC, "kvtc_linalg.cpp"), "-o", o]))

@@ -699,6 +699,9 @@ size_t sink_offset(int32_t n) { return align_up((size_t)std::max(n, 1) * sizeof(
 
 }  // namespace
 
+// The other host translation units report errors through the same thread-local message.
+kvtc_status kvtc::report(kvtc_status st, const char* msg) { return fail(st, msg); }
+
 extern "C" {
 
 const char* kvtc_version(void) { return "kvtc 0.1 gfx950"; }
