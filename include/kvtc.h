@@ -620,8 +620,9 @@ kvtc_status kvtc_page_select(const kvtc_pages* pages, const kvtc_requests* reque
 /* Attention of one new token: for every request and query head
  *   out = sum_t softmax_t(scale q.k_t) v_t,  lse = log sum_t exp(scale q.k_t)
  * over the tokens t < lens[i], or with a selection over those of them in the
- * selected pages (entries below 0 or past the request's pages are left out; a
- * page listed twice counts twice). No tokens: out = 0 and lse = -inf. Rows of
+ * selected pages (of a request with m pages the first min(budget, m) entries
+ * are read; entries below 0 or past its pages are left out, a page listed
+ * twice counts twice). No tokens: out = 0 and lse = -inf. Rows of
  * a page behind lens[i] are never used, whatever they hold. Sums and the
  * softmax's maximum and sum are fp32; out is rounded once. Equal calls give
  * equal bits. */

@@ -34,7 +34,8 @@ def _run(cmd, verbose):
 
 
 # gfx950 kernel translation units (compiled in parallel)
-HIP_SOURCES = ["kvtc_encode.hip", "kvtc_decode.hip", "kvtc_lossless.hip", "kvtc_pages.hip"]
+HIP_SOURCES = ["kvtc_encode.hip", "kvtc_decode.hip", "kvtc_lossless.hip", "kvtc_pages.hip",
+               "kvtc_attend.hip"]
 
 # the host core: the codec, and the checks of the paged-cache calls
 HOST_SOURCES = ["kvtc_host.cpp", "kvtc_pages_host.cpp"]

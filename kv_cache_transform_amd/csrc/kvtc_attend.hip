@@ -1,0 +1,528 @@
+// Attention of one new token over the pages (kvtc_page_attend).
+//
+// For each (request, KV head), G query heads share the keys and values:
+// s = scale K q, p = exp(s - max), out = p V / sum p. Every key and value is
+// read once, for 2 G / element bytes operations a byte, so HBM bounds it.
+//
+// attend_kernel: a fixed number of workgroups each take an equal range of the
+// work, counted in chunks of kAttChunk positions of one row (request, KV head,
+// 16 query heads); the ranges follow from the lengths on the device, so ragged
+// batches stay balanced and a captured graph follows new lengths. Inside a
+// chunk each wave has a tile of positions of its own, loads K and V straight
+// into the registers the matrix instructions read (nothing is shared between
+// waves, so LDS would only add a copy), and keeps its own running maximum and
+// sums; the waves join in LDS at the end of a row's piece. A row that lies in
+// one range is finished there, pieces of the others go to the workspace and
+// join_kernel adds them in a fixed order.
+#include "kvtc_pages_device.h"
+
+namespace kvtc {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int NW = kPageThreads / 64;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+struct AttendArgs {
+  kvtc_pages p;
+  kvtc_requests r;
+  kvtc_queries q;
+  kvtc_selection sel;
+  BlockDiv div;
+  int32_t group;        // query heads per KV head
+  int32_t tiles;        // tiles of 16 query heads per KV head
+  int32_t gt;           // query heads of a full tile
+  float* part;          // pieces of rows, two per workgroup
+  uint4* meta;          // per workgroup: the row that its range starts inside (see join_kernel)
+};
+
+// A piece of a row in the workspace: gt rows of DP sums, gt maxima (base 2),
+// gt sums of weights.
+__host__ __device__ constexpr size_t part_floats(int gt, int dp) { return (size_t)gt * (dp + 2); }
+
+// One wave's tile: positions [P, P + TK) of a row in the lanes' registers,
+// lane l = 16 g + r.
+//
+// bf16, TK = 32, v_mfma_f32_16x16x32_bf16 (16 rows x 32 deep, lane l gives
+// row r, depth 8 g .. + 8): first product S^T = K q^T, two blocks of 16 keys;
+// block t's row r is position 8 (r / 4) + 4 t + r % 4, so that the result,
+// rows 4 g + i of query r, is positions 8 g + 4 t + i: exactly the depths 8 g ..
+// + 8 that the lane gives as the second product's operand. out^T = V^T p^T: the lane loads positions 8 g .. + 8, 16 bytes
+// (dims 8 r .. + 8) of each, whole 256-byte rows per instruction, and transposes
+// 8 x 8 in registers; product j yields dims 8 r' + j of query r in rows r'.
+//
+// f32, TK = 16, v_mfma_f32_16x16x4_f32 (lane gives row r, depth g): key row
+// r is position r, depths in the order the 16-byte loads bring; the result's
+// rows 4 g + i are the positions whose values the lane loads.
+template <class T, int DP> struct Tile;
+
+template <int DP>
+struct Tile<uint16_t, DP> {
+  static constexpr int TK = 32, TG = 8, KS = DP / 32, VB = DP >= 128 ? DP / 128 : 1, VW = DP >= 128 ? 4 : 2, ND = 2 * VW;
+  static constexpr int OUT = VB * ND;                 // accumulators of 4 (out^T)
+  typedef uint32_t vvec __attribute__((ext_vector_type(VW)));
+  u32x4 k[2][KS];
+  vvec v[TG][VB];
+  // the head's elements of the lane's key rows and value rows
+  static constexpr int KR = 2;
+  __device__ __forceinline__ static int key_at(int t, int r) { return 4 * t + (r & 3); }   // of its group
+  template <class KP, class VP>
+  __device__ __forceinline__ void load(KP kp, VP vp, int D, int g, int r) {
+#pragma unroll
+    for (int t = 0; t < KR; ++t)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int d = 32 * s + 8 * g;
+        k[t][s] = *(const u32x4*)(kp(t) + (d < D ? d : 0));
+      }
+#pragma unroll
+    for (int e = 0; e < TG; ++e)
+#pragma unroll
+      for (int b = 0; b < VB; ++b) {
+        const int d = 128 * b + ND * r;
+        v[e][b] = *(const vvec*)(vp(e) + (d < D ? d : 0));
+      }
+  }
+  // dims past D: zero in K (they meet zeros of q, but a NaN must not), never stored from V
+  __device__ __forceinline__ void mask_dims(int D, int g) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      if (32 * s + 8 * g >= D) k[0][s] = k[1][s] = u32x4{0, 0, 0, 0};
+  }
+  // positions whose bit of live is clear are not attended to: their weight is 0, but 0 x NaN is not
+  __device__ __forceinline__ void mask_rows(uint32_t live) {
+#pragma unroll
+    for (int e = 0; e < TG; ++e)
+#pragma unroll
+      for (int b = 0; b < VB; ++b)
+        if (!(live >> e & 1)) v[e][b] = vvec(0);
+  }
+  struct Query {
+    u32x4 f[KS];
+    __device__ __forceinline__ void load(const uint16_t* q, int D, int g, bool there) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int d = 32 * s + 8 * g;
+        f[s] = there && d < D ? *(const u32x4*)(q + d) : u32x4{0, 0, 0, 0};
+      }
+    }
+  };
+  __device__ __forceinline__ void scores(const Query& q, float* s) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+        a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[t][i]), __builtin_bit_cast(bf16x8, q.f[i]), a, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[4 * t + i] = a[i];
+    }
+  }
+  // The weights enter as two bf16 terms: 16 bits of them, where a single
+  // term's 8 would add as much error again as the rounding of a bf16 out; the
+  // matrix units have the time.
+  __device__ __forceinline__ void add_values(const float* p, f32x4* o) const {
+    u32x4 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bf16x2 h = {(__bf16)p[2 * e], (__bf16)p[2 * e + 1]};
+      const bf16x2 l = {(__bf16)(p[2 * e] - (float)h[0]), (__bf16)(p[2 * e + 1] - (float)h[1])};
+      hi[e] = __builtin_bit_cast(uint32_t, h);
+      lo[e] = __builtin_bit_cast(uint32_t, l);
+    }
+#pragma unroll
+    for (int b = 0; b < VB; ++b)
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        u32x4 even, odd;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          even[e] = __builtin_amdgcn_perm(v[2 * e + 1][b][w], v[2 * e][b][w], 0x05040100);
+          odd[e] = __builtin_amdgcn_perm(v[2 * e + 1][b][w], v[2 * e][b][w], 0x07060302);
+        }
+        f32x4& x = o[b * ND + 2 * w];
+        f32x4& y = o[b * ND + 2 * w + 1];
+        x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), __builtin_bit_cast(bf16x8, hi), x, 0, 0, 0);
+        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), __builtin_bit_cast(bf16x8, hi), y, 0, 0, 0);
+        x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), __builtin_bit_cast(bf16x8, lo), x, 0, 0, 0);
+        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), __builtin_bit_cast(bf16x8, lo), y, 0, 0, 0);
+      }
+  }
+};
+
+template <int DP>
+struct Tile<float, DP> {
+  static constexpr int TK = 16, TG = 4, KS = DP / 16, VB = DP / 64, ND = 4;
+  static constexpr int OUT = VB * ND;
+  f32x4 k[KS];
+  f32x4 v[TG][VB];
+  static constexpr int KR = 1;
+  __device__ __forceinline__ static int key_at(int, int r) { return r & 3; }
+  template <class KP, class VP>
+  __device__ __forceinline__ void load(KP kp, VP vp, int D, int g, int r) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int d = 16 * s + 4 * g;
+      k[s] = *(const f32x4*)(kp(0) + (d < D ? d : 0));
+    }
+#pragma unroll
+    for (int e = 0; e < TG; ++e)
+#pragma unroll
+      for (int b = 0; b < VB; ++b) {
+        const int d = 64 * b + ND * r;
+        v[e][b] = *(const f32x4*)(vp(e) + (d < D ? d : 0));
+      }
+  }
+  __device__ __forceinline__ void mask_dims(int D, int g) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      if (16 * s + 4 * g >= D) k[s] = f32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void mask_rows(uint32_t live) {
+#pragma unroll
+    for (int e = 0; e < TG; ++e)
+#pragma unroll
+      for (int b = 0; b < VB; ++b)
+        if (!(live >> e & 1)) v[e][b] = f32x4{0, 0, 0, 0};
+  }
+  struct Query {
+    f32x4 f[KS];
+    __device__ __forceinline__ void load(const float* q, int D, int g, bool there) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int d = 16 * s + 4 * g;
+        f[s] = there && d < D ? *(const f32x4*)(q + d) : f32x4{0, 0, 0, 0};
+      }
+    }
+  };
+  __device__ __forceinline__ void scores(const Query& q, float* s) const {
+    f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};      // two chains: one would wait for each result
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; x += 2) {
+        a = __builtin_amdgcn_mfma_f32_16x16x4f32(k[i][x], q.f[i][x], a, 0, 0, 0);
+        b = __builtin_amdgcn_mfma_f32_16x16x4f32(k[i][x + 1], q.f[i][x + 1], b, 0, 0, 0);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = a[i] + b[i];
+  }
+  __device__ __forceinline__ void add_values(const float* p, f32x4* o) const {
+#pragma unroll
+    for (int e = 0; e < TG; ++e)
+#pragma unroll
+      for (int b = 0; b < VB; ++b)
+#pragma unroll
+        for (int j = 0; j < ND; ++j)
+          o[b * ND + j] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[e][b][j], p[e], o[b * ND + j], 0, 0, 0);
+  }
+};
+
+// max over the four lanes l, l ^ 16, l ^ 32, l ^ 48 (one query's positions); sum likewise
+__device__ __forceinline__ float max_groups(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16, 64));
+  return fmaxf(x, __shfl_xor(x, 32, 64));
+}
+__device__ __forceinline__ float sum_groups(float x) {
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
+
+// A position's row in the pages, and whether it is attended to (bit 0); for
+// whole groups of positions the first one's row and a bit for each.
+struct Place {
+  int64_t row;
+  uint32_t live;
+};
+
+// DP: head_dim rounded up to 64, 128 or 256. GROUPED: every page holds whole
+// groups of TG positions (block_size is a multiple), so a lane looks up two
+// pages a tile and not one for each of its rows.
+template <class T, int DP, bool GROUPED>
+__global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(AttendArgs a) {
+  typedef Tile<T, DP> TT;
+  constexpr int TK = TT::TK, TG = TT::TG, CH = NW * TK, NS = TK / 4;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ uint32_t scan_part[NW];
+  __shared__ float wm[NW][16], wl[NW][16];
+  float* wo = (float*)lds;                                              // [NW][gt][DP]
+  uint32_t* pre = (uint32_t*)(lds + (size_t)NW * a.gt * DP * 4);        // chunks of the requests before each one, per row
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
+  const int n_req = a.r.n_requests, bs = a.p.block_size, D = a.p.head_dim, rows_each = a.p.kv_heads * a.tiles;
+  const int64_t F = (int64_t)a.p.kv_heads * D;
+
+  // positions of request i: its tokens, or those of as many selected pages as it has pages
+  auto positions = [&](int len) -> int {
+    if (!a.sel.blocks) return max(len, 0);
+    return min(a.sel.budget, pages_of(len, bs)) * bs;
+  };
+  uint32_t total;
+  {
+    const int each = (n_req + kPageThreads - 1) / kPageThreads, i0 = threadIdx.x * each;
+    uint32_t mine = 0;
+    for (int i = i0; i < min(i0 + each, n_req); ++i) {
+      const int len = checked_len(a.r, bs, i);
+      if (len < 0 && blockIdx.x == 0) set_status(a.r.status, i, KVTC_E_INVALID);
+      mine += (uint32_t)((positions(len) + CH - 1) / CH);
+    }
+    uint32_t before = scan_threads(mine, scan_part, &total);
+    for (int i = i0; i < min(i0 + each, n_req); ++i) {
+      pre[i] = before;
+      before += (uint32_t)((positions(checked_len(a.r, bs, i)) + CH - 1) / CH);
+    }
+  }
+  __syncthreads();
+  total *= rows_each;
+  const uint32_t per = (total + gridDim.x - 1) / gridDim.x;
+  const uint32_t u0 = min(blockIdx.x * per, total), u1 = min(u0 + per, total);
+  // requests without a token have no chunk
+  for (int i = blockIdx.x * NW + wave; i < n_req; i += gridDim.x * NW)
+    if (checked_len(a.r, bs, i) <= 0) {
+      for (int d = lane; d < a.q.q_heads * D; d += 64) Elem<T>::put((T*)a.q.out + i * a.q.out_stride + d, 0.0f);
+      for (int h = lane; a.q.lse && h < a.q.q_heads; h += 64) a.q.lse[(int64_t)i * a.q.q_heads + h] = -INFINITY;
+    }
+  uint4 meta = {0, 0, 0, 0};
+
+  for (uint32_t u = u0; u < u1;) {
+    // the row: request i, KV head h, query tile qt; its chunks [c0, c1) of n
+    const int i = owner_of(pre, n_req, u / rows_each);
+    const int len = checked_len(a.r, bs, i);
+    const int n_pos = positions(len), n_pages = pages_of(len, bs);
+    const uint32_t n = (uint32_t)((n_pos + CH - 1) / CH), at = u - pre[i] * rows_each, row = at / n;
+    const int h = (int)row / a.tiles, qt = (int)row % a.tiles;
+    const uint32_t c0 = at - row * n, c1 = min(n, c0 + (u1 - u));
+    const int nq = min(16, a.group - 16 * qt);
+    const int32_t* list = a.sel.blocks ? a.sel.blocks + ((int64_t)i * a.p.kv_heads + h) * a.sel.budget : nullptr;
+    const int32_t* table = a.r.block_table + (int64_t)i * a.r.table_stride;
+    const int64_t q_at = ((int64_t)h * a.group + 16 * qt) * D;
+    typename TT::Query q;
+    q.load((const T*)a.q.q + i * a.q.q_stride + q_at + (int64_t)r * D, D, g, r < nq);
+    const float c = a.q.scale * kLog2e;
+    float m = -INFINITY, l = 0.0f;
+    f32x4 o[TT::OUT];
+#pragma unroll
+    for (int j = 0; j < TT::OUT; ++j) o[j] = f32x4{0, 0, 0, 0};
+
+    auto place = [&](int pos) -> Place {
+      Place w = {0, 0};
+      if (pos >= n_pos) return w;
+      const uint32_t slot = div_block(pos, a.div);
+      const int off = pos - (int)slot * bs;
+      const int j = list ? list[slot] : (int)slot;
+      if (j < 0 || j >= n_pages) return w;
+      const int id = table[j];
+      if (id < 0 || id >= a.p.n_blocks) {
+        set_status(a.r.status, i, KVTC_E_INVALID);
+        return w;
+      }
+      w.row = (int64_t)id * bs + off;
+      const int left = len - (j * bs + off);       // tokens from here on
+      if (GROUPED) w.live = left >= TG ? (1u << TG) - 1 : left > 0 ? (1u << left) - 1 : 0u;
+      else w.live = left > 0;
+      return w;
+    };
+    const T* kh = (const T*)a.p.k + h * D;
+    const T* vh = (const T*)a.p.v + h * D;
+    for (uint32_t ch = c0; ch < c1; ++ch) {
+      const int P = (int)ch * CH + wave * TK, kg = P + TG * (r >> 2), vg = P + TG * g;
+      TT t;
+      uint32_t live = 0;       // of the value group, which is the score group too
+      if constexpr (GROUPED) {
+        const Place kw = place(kg), vw = place(vg);
+        const T* kp = kh + kw.row * F;
+        const T* vp = vh + vw.row * F;
+        t.load([&](int x) { return kp + TT::key_at(x, r) * F; }, [&](int e) { return vp + e * F; }, D, g, r);
+        live = vw.live;
+      } else {
+        int64_t kr[TT::KR], vr[TG];
+#pragma unroll
+        for (int x = 0; x < TT::KR; ++x) kr[x] = place(kg + TT::key_at(x, r)).row;
+#pragma unroll
+        for (int e = 0; e < TG; ++e) {
+          const Place w = place(vg + e);
+          vr[e] = w.row;
+          live |= w.live << e;
+        }
+        t.load([&](int x) { return kh + kr[x] * F; }, [&](int e) { return vh + vr[e] * F; }, D, g, r);
+      }
+      if (D != DP) t.mask_dims(D, g);
+      float s[NS];
+      t.scores(q, s);
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < NS; ++e) {
+        s[e] = live >> e & 1 ? s[e] * c : -INFINITY;
+        top = fmaxf(top, s[e]);
+      }
+      t.mask_rows(live);
+      top = fmaxf(m, max_groups(top));
+      const float base = top == -INFINITY ? 0.0f : top;
+      const float f = __builtin_amdgcn_exp2f(m - base);
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < TT::OUT; ++j) o[j] *= f;
+#pragma unroll
+      for (int e = 0; e < NS; ++e) {
+        s[e] = __builtin_amdgcn_exp2f(s[e] - base);
+        l += s[e];
+      }
+      t.add_values(s, o);
+    }
+
+    // join the waves
+    l = sum_groups(l);
+    if (g == 0) {
+      wm[wave][r] = m;
+      wl[wave][r] = l;
+    }
+    __syncthreads();
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w][r]);
+    const float f = __builtin_amdgcn_exp2f(m - (M == -INFINITY ? 0.0f : M));
+    if (r < nq) {
+#pragma unroll
+      for (int b = 0; b < TT::VB; ++b)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int j = 0; j < TT::ND; ++j)
+            wo[((size_t)wave * a.gt + r) * DP + b * 16 * TT::ND + (4 * g + x) * TT::ND + j] = o[b * TT::ND + j][x] * f;
+    }
+    __syncthreads();
+    const bool whole = c0 == 0 && c1 == n;
+    float* part = a.part + (2 * (size_t)blockIdx.x + (c0 ? 0 : 1)) * part_floats(a.gt, DP);
+    for (int x = threadIdx.x; x < nq * (DP / 4); x += kPageThreads) {
+      const int qr = x / (DP / 4), d = x % (DP / 4) * 4;
+      f32x4 v = {0, 0, 0, 0};
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, wm[w][qr]);
+      const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        v += *(const f32x4*)(wo + ((size_t)w * a.gt + qr) * DP + d);
+        sum += wl[w][qr] * __builtin_amdgcn_exp2f(wm[w][qr] - base);
+      }
+      if (whole) {
+        const float z = sum == 0.0f ? 0.0f : 1.0f / sum;
+        T* out = (T*)a.q.out + i * a.q.out_stride + q_at + (int64_t)qr * D + d;
+        if (d < D)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) Elem<T>::put(out + e, v[e] * z);
+        if (d == 0 && a.q.lse)
+          a.q.lse[(int64_t)i * a.q.q_heads + (int64_t)h * a.group + 16 * qt + qr] =
+              sum == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(sum)) * kLn2;
+      } else {
+        *(f32x4*)(part + (size_t)qr * DP + d) = v;
+        if (d == 0) {
+          part[(size_t)a.gt * DP + qr] = top;
+          part[(size_t)a.gt * (DP + 1) + qr] = sum;
+        }
+      }
+    }
+    // The range starts inside this row, and the row began in the range before: this workgroup's entry tells
+    // join_kernel the row and the last range it reaches.
+    if (u == u0 && c0 > 0 && c0 <= per)
+      meta = uint4{1u + (uint32_t)i, row, (u - c0 + n - 1) / per, 0};
+    __syncthreads();
+    u += c1 - c0;
+  }
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = meta;
+}
+
+// Adds the pieces of one row and query head: workgroup (w, query) does so if
+// range w is the second that the row reaches. Pieces lie in slot 1 of range
+// w - 1 and slot 0 of ranges w .. last.
+template <class T, int DP>
+__global__ void __launch_bounds__(kPageThreads) join_kernel(AttendArgs a) {
+  constexpr int LANES = DP / 4, PER = kPageThreads / LANES;     // threads on one piece, pieces at a time
+  __shared__ f32x4 sums[PER][LANES];
+  __shared__ float tops[NW], weights[PER];
+  const uint4 meta = a.meta[blockIdx.x];
+  const int i = (int)meta.x - 1, h = (int)meta.y / a.tiles, qt = (int)meta.y % a.tiles, qr = blockIdx.y;
+  if (i < 0 || qr >= min(16, a.group - 16 * qt)) return;
+  const int w0 = (int)blockIdx.x - 1, n = (int)meta.z - w0 + 1, D = a.p.head_dim;
+  auto piece = [&](int x) { return a.part + (2 * (size_t)(w0 + x) + (x ? 0 : 1)) * part_floats(a.gt, DP); };
+  float top = -INFINITY;
+  for (int x = threadIdx.x; x < n; x += kPageThreads) top = fmaxf(top, piece(x)[(size_t)a.gt * DP + qr]);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) top = fmaxf(top, tops[w]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  const int d = threadIdx.x % LANES, y = threadIdx.x / LANES;
+  f32x4 v = {0, 0, 0, 0};
+  float sum = 0.0f;
+  for (int x = y; x < n; x += PER) {
+    const float* p = piece(x);
+    const float f = __builtin_amdgcn_exp2f(p[(size_t)a.gt * DP + qr] - base);
+    sum += f * p[(size_t)a.gt * (DP + 1) + qr];
+    v += f * *(const f32x4*)(p + (size_t)qr * DP + 4 * d);
+  }
+  sums[y][d] = v;
+  if (d == 0) weights[y] = sum;
+  __syncthreads();
+  if (y) return;
+  sum = 0.0f;
+  v = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    v += sums[x][d];
+    sum += weights[x];
+  }
+  const float z = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t hq = (int64_t)h * a.group + 16 * qt + qr;
+  T* out = (T*)a.q.out + i * a.q.out_stride + hq * D + 4 * d;
+  if (4 * d < D)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Elem<T>::put(out + e, v[e] * z);
+  if (d == 0 && a.q.lse)
+    a.q.lse[(int64_t)i * a.q.q_heads + hq] = sum == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <class T, int DP, bool GROUPED>
+void launch_pieces(const AttendArgs& a, uint32_t grid, hipStream_t s) {
+  const size_t lds = (size_t)NW * a.gt * DP * 4 + (size_t)a.r.n_requests * 4;
+  allow_lds(attend_kernel<T, DP, GROUPED>, lds);
+  hipLaunchKernelGGL((attend_kernel<T, DP, GROUPED>), dim3(grid), dim3(kPageThreads), lds, s, a);
+}
+
+template <class T, int DP>
+int launch(const AttendArgs& a, uint32_t grid, hipStream_t s) {
+  if (a.p.block_size % Tile<T, DP>::TG == 0) launch_pieces<T, DP, true>(a, grid, s);
+  else launch_pieces<T, DP, false>(a, grid, s);
+  if (grid > 1)
+    hipLaunchKernelGGL((join_kernel<T, DP>), dim3(grid, a.gt), dim3(kPageThreads), 0, s, a);
+  return (int)hipGetLastError();
+}
+
+}  // namespace
+
+int launch_page_attend(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q, const kvtc_selection& sel,
+                       void* ws, hipStream_t s) {
+  AttendArgs a;
+  a.p = p;
+  a.r = r;
+  a.q = q;
+  a.sel = sel;
+  a.div = block_div(p.block_size);
+  a.group = q.q_heads / p.kv_heads;
+  a.tiles = (a.group + 15) / 16;
+  a.gt = std::min(a.group, 16);
+  a.meta = (uint4*)ws;
+  a.part = (float*)((uint8_t*)ws + attend_meta_bytes());
+  const uint32_t grid = attend_workers(p, r, q);
+  const int D = p.head_dim;
+  if (p.dtype == KVTC_F32)
+    return D <= 64 ? launch<float, 64>(a, grid, s) : D <= 128 ? launch<float, 128>(a, grid, s) : launch<float, 256>(a, grid, s);
+  return D <= 64 ? launch<uint16_t, 64>(a, grid, s) : D <= 128 ? launch<uint16_t, 128>(a, grid, s) : launch<uint16_t, 256>(a, grid, s);
+}
+
+}  // namespace kvtc

@@ -15,6 +15,30 @@ __host__ __device__ inline size_t select_ws_bytes(const kvtc_pages& p, const kvt
   return align_up((size_t)r.n_requests * p.kv_heads * r.table_width * 4, kAlign);
 }
 
+// kvtc_page_attend: positions per chunk of work (four waves' tiles), head_dim
+// as the kernels round it up, and the number of workgroups: two for each of
+// the 256 CUs, or as many as there can be chunks. Sizes alone decide, so that
+// a workspace can be sized without a device.
+constexpr int kAttendWorkers = 512;
+__host__ __device__ inline int attend_chunk(int dtype) { return dtype == KVTC_F32 ? 64 : 128; }
+__host__ __device__ inline int attend_dp(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+inline int64_t attend_most_chunks(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q) {
+  const int64_t ch = attend_chunk(p.dtype), rows = (int64_t)p.kv_heads * ((q.q_heads / p.kv_heads + 15) / 16);
+  return r.n_requests * rows * (((int64_t)r.table_width * p.block_size + ch - 1) / ch);
+}
+inline uint32_t attend_workers(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q) {
+  const int64_t n = attend_most_chunks(p, r, q);
+  return (uint32_t)(n < kAttendWorkers ? n : kAttendWorkers);
+}
+// Workspace: an entry per workgroup, then two pieces of rows per workgroup
+// (up to 16 query heads' sums, maxima and weights).
+inline size_t attend_meta_bytes() { return align_up((size_t)kAttendWorkers * 16, kAlign); }
+inline size_t attend_ws_bytes(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q) {
+  const int group = q.q_heads / p.kv_heads, gt = group < 16 ? group : 16;
+  return attend_meta_bytes() +
+         align_up((size_t)attend_workers(p, r, q) * 2 * gt * (attend_dp(p.head_dim) + 2) * 4, kAlign);
+}
+
 // Every launcher returns a hipError_t value cast to int.
 int launch_page_tables(const kvtc_page_plan& a, hipStream_t s);
 int launch_page_write(const kvtc_pages& p, const kvtc_page_rows& r, hipStream_t s);

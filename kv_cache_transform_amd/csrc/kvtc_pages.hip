@@ -1,69 +1,10 @@
 // Kernels of the paged-cache calls: block tables and slot maps, the write of
-// new rows, key bounds per page, the selection of pages by a score on those
-// bounds, and attention of one new token over the pages.
-#include "kvtc_device.h"
-#include "kvtc_pages.h"
+// new rows, key bounds per page, and the selection of pages by a score on
+// those bounds. (Attention over the pages: kvtc_attend.hip.)
+#include "kvtc_pages_device.h"
 
 namespace kvtc {
 namespace {
-
-template <class T> struct Elem;
-template <> struct Elem<float> {
-  static __device__ __forceinline__ float get(const float* p) { return *p; }
-  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
-};
-template <> struct Elem<uint16_t> {
-  static __device__ __forceinline__ float get(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-  // round to nearest even; a NaN stays one
-  static __device__ __forceinline__ void put(uint16_t* p, float v) {
-    *p = v != v ? (uint16_t)0x7FC0u : (uint16_t)bf16_bits_rne(v);
-  }
-};
-
-// Tokens of request i that a call attends to, or -1 for a length that the
-// table cannot hold.
-__device__ __forceinline__ int checked_len(const kvtc_requests& r, int block_size, int i) {
-  const int n = r.lens[i];
-  return n < 0 || n > r.table_width * block_size ? -1 : n;
-}
-__device__ __forceinline__ int pages_of(int tokens, int block_size) {
-  return tokens > 0 ? (tokens - 1) / block_size + 1 : 0;
-}
-__device__ __forceinline__ void set_status(int32_t* status, int i, int st) {
-  if (status) status[i] = st;
-}
-
-// Exclusive scan of v over the workgroup's kPageThreads threads; the total in
-// *sum. part: kPageThreads / 64 words of LDS.
-__device__ __forceinline__ uint64_t scan_threads(uint64_t v, uint64_t* part, uint64_t* sum) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint64_t x = v;
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
-  }
-  __syncthreads();
-  if (lane == 63) part[wave] = x;
-  __syncthreads();
-  uint64_t before = 0, all = 0;
-  for (int w = 0; w < kPageThreads / 64; ++w) {
-    if (w < wave) before += part[w];
-    all += part[w];
-  }
-  *sum = all;
-  return before + x - v;
-}
-
-// The last index i in [0, n) with first[i] <= x (first[0] = 0, ascending).
-__device__ __forceinline__ int owner_of(const uint32_t* first, int n, uint32_t x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= x) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
 
 // ------------------------------------------------- block tables, slot maps ---
 
@@ -94,7 +35,7 @@ __global__ void __launch_bounds__(kPageThreads) tables_kernel(kvtc_page_plan a) 
     const uint64_t t0 = tokens + scan_threads(grow, part, &sum_t);
     const uint64_t p0 = needed + scan_threads(need, part, &sum_p);
     const bool fits = t0 + grow <= (uint64_t)a.n_slots && (need == 0 || from + p0 + need <= (uint64_t)a.n_free);
-    scan_threads(ok && fits ? need : 0, part, &sum_g);
+    scan_threads(ok && fits ? need : (uint64_t)0, part, &sum_g);
     if (i < a.n_requests) {
       start[i] = (uint32_t)min(t0, kCap);
       page[i] = (uint32_t)min(p0, kCap);
@@ -274,79 +215,14 @@ __global__ void __launch_bounds__(kPageThreads) select_kernel(kvtc_pages p, kvtc
     const uint32_t k = j < n ? key[j] : 0u;
     const bool tie = k && k == least;
     uint64_t sum;
-    const uint64_t before = tied + scan_threads(tie, part, &sum);
+    const uint64_t before = tied + scan_threads((uint64_t)tie, part, &sum);
     tied += sum;
     const bool take = k && (k > least || (tie && before < ties));
-    const uint64_t at = done + scan_threads(take, part, &sum);
+    const uint64_t at = done + scan_threads((uint64_t)take, part, &sum);
     done += sum;
     if (take) out[at] = j;
   }
   for (int j = (int)done + (int)threadIdx.x; j < sel.budget; j += kPageThreads) out[j] = -1;
-}
-
-// ---------------------------------------------------------------- attention ---
-
-// One workgroup per (query head, request); each wave takes every fourth token
-// with a running maximum and sum, and the four are joined in LDS.
-template <class T>
-__global__ void __launch_bounds__(kPageThreads) attend_kernel(kvtc_pages p, kvtc_requests r, kvtc_queries q, kvtc_selection sel) {
-  constexpr int NW = kPageThreads / 64;
-  __shared__ float part[NW][KVTC_MAX_HEAD_DIM], mx[NW], sm[NW];
-  const int hq = blockIdx.x, i = blockIdx.y, bs = p.block_size, D = p.head_dim, F = p.kv_heads * D;
-  const int h = hq / (q.q_heads / p.kv_heads), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int len = checked_len(r, bs, i);
-  if (len < 0) {
-    if (threadIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
-    len = 0;
-  }
-  float x[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0;
-  for (int c = 0; c < 4; ++c) {
-    const int d = lane + 64 * c;
-    x[c] = d < D ? Elem<T>::get((const T*)q.q + i * q.q_stride + (int64_t)hq * D + d) : 0.0f;
-  }
-  const int32_t* list = sel.blocks ? sel.blocks + ((int64_t)i * p.kv_heads + h) * sel.budget : nullptr;
-  const int64_t n = list ? (int64_t)sel.budget * bs : len;
-  for (int64_t t = wave; t < n; t += NW) {
-    int64_t j = t / bs;
-    const int off = t % bs;
-    if (list) j = list[j];
-    if (j < 0 || j * bs + off >= len) continue;
-    const int id = r.block_table[(int64_t)i * r.table_stride + j];
-    if (id < 0 || id >= p.n_blocks) {
-      if (lane == 0) set_status(r.status, i, KVTC_E_INVALID);
-      continue;
-    }
-    const int64_t row = ((int64_t)id * bs + off) * F + h * D;
-    float s = 0;
-    for (int c = 0; c < 4; ++c)
-      if (lane + 64 * c < D) s = fmaf(x[c], Elem<T>::get((const T*)p.k + row + lane + 64 * c), s);
-    for (int w = 32; w; w >>= 1) s += __shfl_xor(s, w, 64);
-    s *= q.scale;
-    const float top = fmaxf(m, s), base = top == -INFINITY ? 0.0f : top;
-    const float f = expf(m - base), e = expf(s - base);
-    l = l * f + e;
-    m = top;
-    for (int c = 0; c < 4; ++c)
-      if (lane + 64 * c < D) o[c] = o[c] * f + e * Elem<T>::get((const T*)p.v + row + lane + 64 * c);
-  }
-  if (lane == 0) {
-    mx[wave] = m;
-    sm[wave] = l;
-  }
-  for (int c = 0; c < 4; ++c)
-    if (lane + 64 * c < D) part[wave][lane + 64 * c] = o[c];
-  __syncthreads();
-  float top = -INFINITY;
-  for (int w = 0; w < NW; ++w) top = fmaxf(top, mx[w]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0;
-  for (int w = 0; w < NW; ++w) sum += sm[w] * expf(mx[w] - base);
-  for (int d = threadIdx.x; d < D; d += kPageThreads) {
-    float v = 0;
-    for (int w = 0; w < NW; ++w) v += part[w][d] * expf(mx[w] - base);
-    Elem<T>::put((T*)q.out + i * q.out_stride + (int64_t)hq * D + d, sum == 0.0f ? 0.0f : v / sum);
-  }
-  if (q.lse && threadIdx.x == 0) q.lse[(int64_t)i * q.q_heads + hq] = sum == 0.0f ? -INFINITY : logf(sum) + base;
 }
 
 int grid_for(int64_t n, int most) { return (int)std::min<int64_t>(std::max<int64_t>(n, 1), most); }
@@ -389,17 +265,6 @@ int launch_page_select(const kvtc_pages& p, const kvtc_requests& r, const kvtc_q
     hipLaunchKernelGGL(select_kernel<float>, grid, dim3(kPageThreads), 0, s, p, r, q, (const float*)bounds, sel, (uint32_t*)ws);
   else
     hipLaunchKernelGGL(select_kernel<uint16_t>, grid, dim3(kPageThreads), 0, s, p, r, q, (const uint16_t*)bounds, sel, (uint32_t*)ws);
-  return (int)hipGetLastError();
-}
-
-int launch_page_attend(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q, const kvtc_selection& sel,
-                       void* ws, hipStream_t s) {
-  (void)ws;
-  const dim3 grid(q.q_heads, r.n_requests);
-  if (p.dtype == KVTC_F32)
-    hipLaunchKernelGGL(attend_kernel<float>, grid, dim3(kPageThreads), 0, s, p, r, q, sel);
-  else
-    hipLaunchKernelGGL(attend_kernel<uint16_t>, grid, dim3(kPageThreads), 0, s, p, r, q, sel);
   return (int)hipGetLastError();
 }
 

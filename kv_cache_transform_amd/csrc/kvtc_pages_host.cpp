@@ -79,7 +79,8 @@ kvtc_status check_requests(const kvtc_requests* r, const kvtc_pages& p, bool dat
   return KVTC_OK;
 }
 
-kvtc_status check_queries(const kvtc_queries* q, const kvtc_pages& p, bool out, bool data, kvtc_queries* dense) {
+kvtc_status check_queries(const kvtc_queries* q, const kvtc_pages& p, const kvtc_requests& r, bool out, bool data,
+                          kvtc_queries* dense) {
   if (!q) return report(KVTC_E_INVALID, "null queries");
   if (q->q_heads <= 0 || q->q_heads % p.kv_heads || q->q_heads > 65535)
     return report(KVTC_E_INVALID, "queries: q_heads must be a positive multiple of kv_heads below 2^16");
@@ -89,6 +90,8 @@ kvtc_status check_queries(const kvtc_queries* q, const kvtc_pages& p, bool out, 
   if (!dense->out_stride) dense->out_stride = row;
   if (dense->q_stride < row || dense->q_stride % 8 || (out && (dense->out_stride < row || dense->out_stride % 8)))
     return report(KVTC_E_INVALID, "queries: strides must cover a row and be multiples of 8");
+  if (attend_most_chunks(p, r, *q) >= (int64_t)INT32_MAX)
+    return report(KVTC_E_UNSUPPORTED, "requests * heads * tokens of the tables past the kernels' 2^31 chunks");
   if (!data) return KVTC_OK;
   if (!q->q || !aligned16(q->q) || (out && (!q->out || !aligned16(q->out) || !aligned4(q->lse))))
     return report(KVTC_E_INVALID, "queries: q and out must be non-null and 16-byte aligned");
@@ -112,8 +115,8 @@ kvtc_status check_workspace(const void* ws, size_t have, size_t need) {
 }
 
 size_t workspace_bytes(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q, const kvtc_selection* s) {
-  (void)q;
-  return (s ? select_ws_bytes(p, r) : 0) + kAlign;
+  const size_t a = attend_ws_bytes(p, r, q), b = s ? select_ws_bytes(p, r) : 0;
+  return a > b ? a : b;
 }
 
 }  // namespace
@@ -171,7 +174,7 @@ size_t kvtc_page_workspace_bytes(const kvtc_pages* p, const kvtc_requests* r, co
                                  const kvtc_selection* s) {
   kvtc_queries dense;
   if (check_pages(p, false, false) != KVTC_OK || check_requests(r, *p, false) != KVTC_OK ||
-      check_queries(q, *p, false, false, &dense) != KVTC_OK || (s && check_selection(s, false, false) != KVTC_OK))
+      check_queries(q, *p, *r, false, false, &dense) != KVTC_OK || (s && check_selection(s, false, false) != KVTC_OK))
     return 0;
   return workspace_bytes(*p, *r, dense, s);
 }
@@ -182,7 +185,7 @@ kvtc_status kvtc_page_select(const kvtc_pages* p, const kvtc_requests* r, const 
   kvtc_queries dense;
   kvtc_status st = check_pages(p, false, false);
   if (st == KVTC_OK) st = check_requests(r, *p, true);
-  if (st == KVTC_OK) st = check_queries(q, *p, false, true, &dense);
+  if (st == KVTC_OK) st = check_queries(q, *p, *r, false, true, &dense);
   if (st != KVTC_OK) return st;
   if (!s) return report(KVTC_E_INVALID, "null selection");
   st = check_selection(s, true, true);
@@ -201,7 +204,7 @@ kvtc_status kvtc_page_attend(const kvtc_pages* p, const kvtc_requests* r, const 
   kvtc_queries dense;
   kvtc_status st = check_pages(p, true, true);
   if (st == KVTC_OK) st = check_requests(r, *p, true);
-  if (st == KVTC_OK) st = check_queries(q, *p, true, true, &dense);
+  if (st == KVTC_OK) st = check_queries(q, *p, *r, true, true, &dense);
   if (st == KVTC_OK && s) st = check_selection(s, false, true);
   if (st == KVTC_OK) st = check_workspace(d_ws, ws_bytes, workspace_bytes(*p, *r, dense, nullptr));
   if (st != KVTC_OK) return st;
