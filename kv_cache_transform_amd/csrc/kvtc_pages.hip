@@ -148,81 +148,203 @@ __device__ __forceinline__ uint32_t score_key(double s) {
   return f != f ? kKeyNan : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// One workgroup per (KV head, request): a wave scores a page at a time, then
-// the threshold is found bit by bit and the pages above it listed in order.
+// Scores of the pages [blockIdx.x * span, + span) of request blockIdx.z for KV
+// head blockIdx.y. LP lanes (a power of two) share a page, 16 bytes of each
+// bound to a lane, so a load instruction covers whole 16 * LP byte rows; each
+// lane keeps its dims' two query sums in fp64. Reading the bounds is what
+// it costs: about 60 vector instructions for 2 KB a wave are a third of the
+// time that HBM takes for them.
 template <class T>
-__global__ void __launch_bounds__(kPageThreads) select_kernel(kvtc_pages p, kvtc_requests r, kvtc_queries q, const T* bounds, kvtc_selection sel, uint32_t* keys) {
-  __shared__ uint64_t part[kPageThreads / 64];
-  __shared__ double up[KVTC_MAX_HEAD_DIM], down[KVTC_MAX_HEAD_DIM];
-  const int h = blockIdx.x, i = blockIdx.y, bs = p.block_size, D = p.head_dim, F = p.kv_heads * D;
-  const int G = q.q_heads / p.kv_heads, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int len = checked_len(r, bs, i);
-  if (len < 0) {
-    if (threadIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
-    len = 0;
-  }
-  const int n = pages_of(len, bs);
-  for (int d = threadIdx.x; d < D; d += kPageThreads) {
-    double u = 0, w = 0;
-    for (int g = 0; g < G; ++g) {
-      const float x = Elem<T>::get((const T*)q.q + i * q.q_stride + (int64_t)(h * G + g) * D + d);
-      // (a NaN enters both sums)
-      u += x < 0 ? 0.0 : (double)x;
-      w += x > 0 ? 0.0 : (double)x;
+__global__ void __launch_bounds__(kPageThreads) score_kernel(kvtc_pages p, kvtc_requests r, kvtc_queries q, const T* bounds,
+                                                             kvtc_selection sel, uint32_t* keys, int span, int LP) {
+  constexpr int EL = 16 / sizeof(T);
+  typedef T row16 __attribute__((ext_vector_type(EL)));
+  const int h = blockIdx.y, i = blockIdx.z, bs = p.block_size, D = p.head_dim, F = p.kv_heads * D;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d0 = (lane & (LP - 1)) * EL;
+  const int len = checked_len(r, bs, i), n = pages_of(len, bs), j0 = (int)blockIdx.x * span;
+  if (len < 0 && j0 == 0 && h == 0 && threadIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
+  if (j0 >= n) return;
+  const int j1 = min(n, j0 + span);
+  const bool there = d0 < D, all = n <= sel.budget;     // all: every page is selected, whatever its score
+  double up[EL], down[EL];
+#pragma unroll
+  for (int e = 0; e < EL; ++e) up[e] = down[e] = 0.0;
+  const int G = q.q_heads / p.kv_heads;
+  const T* qh = (const T*)q.q + i * q.q_stride + (int64_t)h * G * D + (there ? d0 : 0);
+  for (int g = 0; g < G && !all; ++g) {
+    const row16 x = *(const row16*)(qh + (int64_t)g * D);
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+      const T xe = x[e];
+      const float v = Elem<T>::get(&xe);
+      up[e] += v < 0 ? 0.0 : (double)v;         // (a NaN enters both sums)
+      down[e] += v > 0 ? 0.0 : (double)v;
     }
-    up[d] = u;
-    down[d] = w;
   }
-  __syncthreads();
   uint32_t* key = keys + ((int64_t)i * p.kv_heads + h) * r.table_width;
-  for (int j = wave; j < n; j += kPageThreads / 64) {
-    const int id = r.block_table[(int64_t)i * r.table_stride + j];
+  const int32_t* table = r.block_table + (int64_t)i * r.table_stride;
+  const int step = kPageThreads / LP;
+  for (int base = j0; base < j1; base += step) {
+    const int j = base + (int)threadIdx.x / LP;
+    const int id = j < j1 ? table[j] : -1;
     const bool ok = id >= 0 && id < p.n_blocks;
-    double s = 0;
-    if (ok)
-      for (int d = lane; d < D; d += 64) {
-        const T* b = bounds + (int64_t)id * 2 * F + h * D + d;
-        s += up[d] * (double)Elem<T>::get(b + F) + down[d] * (double)Elem<T>::get(b);
+    const bool keep = all || j < sel.first || j >= n - sel.last;
+    double s0 = 0.0, s1 = 0.0;
+    if (ok && !keep && there) {
+      const T* b = bounds + (int64_t)id * 2 * F + h * D + d0;
+      const row16 lo = *(const row16*)b, hi = *(const row16*)(b + F);
+#pragma unroll
+      for (int e = 0; e < EL; ++e) {
+        const T le = lo[e], he = hi[e];
+        s0 = fma(down[e], (double)Elem<T>::get(&le), s0);
+        s1 = fma(up[e], (double)Elem<T>::get(&he), s1);
       }
-    for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m, 64);
-    if (lane == 0) {
-      key[j] = !ok ? 0u : j < sel.first || j >= n - sel.last ? kKeyKeep : score_key(s);
+    }
+    s0 += s1;
+    for (int m = LP >> 1; m; m >>= 1) s0 += __shfl_xor(s0, m, 64);
+    if (j < j1 && (lane & (LP - 1)) == 0) {
+      key[j] = !ok ? 0u : keep ? kKeyKeep : score_key(s0);
       if (!ok) set_status(r.status, i, KVTC_E_INVALID);
     }
   }
+}
+
+// The pages of the highest keys, in ascending order: one workgroup per (KV
+// head, request). The threshold is found by counting digits of kDigit bits,
+// the first over the range that the keys really span, so that they spread
+// over the counters (their leading bits, sign and exponent, hardly differ);
+// each further digit only among the keys that share those before it. A
+// thread has kOwn consecutive keys, in registers for the first kOwn *
+// kPickThreads pages; past them they are read again for every digit.
+constexpr int kPickThreads = 1024, kOwn = 8, kDigit = 11;
+
+template <class V>
+__device__ __forceinline__ V scan_picks(V v, V* part, V* sum) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  V x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const V y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
   __syncthreads();
-  // the largest threshold that at least `budget` keys reach (0 with fewer)
-  uint32_t least = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t t = least | (1u << bit);
-    uint64_t mine = 0, all;
-    for (int j = threadIdx.x; j < n; j += kPageThreads) mine += key[j] >= t;
-    scan_threads(mine, part, &all);
-    if (all >= (uint64_t)sel.budget) least = t;
+  if (lane == 63) part[wave] = x;
+  __syncthreads();
+  V before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kPickThreads / 64; ++w) {
+    const V y = part[w];
+    if (w < wave) before += y;
+    all += y;
   }
-  uint64_t above = 0;
-  {
-    uint64_t mine = 0;
-    for (int j = threadIdx.x; j < n; j += kPageThreads) mine += key[j] > least;
-    scan_threads(mine, part, &above);
-  }
-  // those above it, and of those at it the first ones
-  const uint64_t ties = least ? sel.budget - above : 0;
+  *sum = all;
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_requests r, kvtc_selection sel, const uint32_t* keys) {
+  __shared__ uint32_t count[1 << kDigit], part[kPickThreads / 64], found[2], range[2];
+  const int h = blockIdx.x, i = blockIdx.y, bs = p.block_size, tid = threadIdx.x;
+  const int n = pages_of(checked_len(r, bs, i), bs), span = kOwn * kPickThreads;
+  const uint32_t* key = keys + ((int64_t)i * p.kv_heads + h) * r.table_width;
   int32_t* out = sel.blocks + ((int64_t)i * p.kv_heads + h) * sel.budget;
-  uint64_t done = 0, tied = 0;
-  for (int base = 0; base < n; base += kPageThreads) {
-    const int j = base + (int)threadIdx.x;
-    const uint32_t k = j < n ? key[j] : 0u;
-    const bool tie = k && k == least;
-    uint64_t sum;
-    const uint64_t before = tied + scan_threads((uint64_t)tie, part, &sum);
-    tied += sum;
-    const bool take = k && (k > least || (tie && before < ties));
-    const uint64_t at = done + scan_threads((uint64_t)take, part, &sum);
-    done += sum;
-    if (take) out[at] = j;
+  uint32_t own[kOwn];
+  auto read = [&](int base) {      // this thread's keys of pages [base, base + span)
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+      const int j = base + tid * kOwn + x;
+      own[x] = j < n ? key[j] : 0u;
+    }
+  };
+  auto each = [&](auto f) {        // f(key) for every key of this thread
+    for (int base = 0; base < n; base += span) {
+      if (base || n > span) read(base);
+#pragma unroll
+      for (int x = 0; x < kOwn; ++x) f(own[x]);
+    }
+  };
+  read(0);
+  // Only keys between those that are never taken and those that always are
+  // can be the threshold; is there a choice at all?
+  if (tid < 2) range[tid] = tid ? 0u : 0xFFFFFFFFu;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u, valid = 0, kept = 0;
+  each([&](uint32_t k) {
+    valid += k != 0;
+    kept += k == kKeyKeep;
+    if (k && k != kKeyKeep) {
+      lo = min(lo, k);
+      hi = max(hi, k);
+    }
+  });
+  uint32_t n_valid, n_kept;
+  scan_picks(valid, part, &n_valid);
+  scan_picks(kept, part, &n_kept);
+  uint32_t least = 1, ties = 0;       // taken: keys above least, and the first `ties` at it
+  if (n_valid > (uint32_t)sel.budget) {
+    atomicMin(&range[0], lo);
+    atomicMax(&range[1], hi);
+    uint32_t want = sel.budget - n_kept;       // of the keys in [lo, hi], the host has seen to want >= 0
+    __syncthreads();
+    lo = range[0];
+    hi = range[1];
+    if (want == 0) {
+      least = kKeyNan;
+      ties = 0;
+    } else {
+      // the keys in question are lo + [0, 2^bits)
+      int bits = 32 - __clz((int)max(hi - lo, 1u));
+      for (;;) {
+        const int low = max(bits - kDigit, 0);
+        for (int x = tid; x < 1 << kDigit; x += kPickThreads) count[x] = 0;
+        __syncthreads();
+        const uint32_t top = hi - lo;
+        each([&](uint32_t k) {
+          if (k >= lo && k - lo <= top && k != kKeyKeep) atomicAdd(&count[(k - lo) >> low], 1u);
+        });
+        __syncthreads();
+        // from the highest digit down: thread t holds digits 2 (last - t) + 1 and 2 (last - t)
+        const int x = 2 * (kPickThreads - 1 - tid);
+        const uint32_t b = count[x + 1], a = count[x];
+        uint32_t sum;
+        const uint32_t above = scan_picks(a + b, part, &sum);
+        if (above < want && want <= above + a + b) {
+          const bool second = want > above + b;
+          found[0] = x + (second ? 0 : 1);
+          found[1] = want - above - (second ? b : 0);
+        }
+        __syncthreads();
+        lo += found[0] << low;
+        want = found[1];
+        if (low == 0) break;
+        hi = min(hi, lo + ((1u << low) - 1));
+        bits = low;
+        __syncthreads();
+      }
+      least = lo;
+      ties = want;
+    }
   }
-  for (int j = (int)done + (int)threadIdx.x; j < sel.budget; j += kPageThreads) out[j] = -1;
+  // 16 bits each: taken for sure, and ties, of this thread's keys of one span
+  uint32_t done = 0, tied = 0;
+  for (int base = 0; base < n; base += span) {
+    if (base || n > span) read(base);
+    uint32_t mine = 0;
+    const bool every = n_valid <= (uint32_t)sel.budget;
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) mine += every ? (own[x] != 0) : (own[x] > least ? 1u : 0u) + (own[x] == least ? 1u << 16 : 0u);
+    uint32_t sum;
+    const uint32_t before = scan_picks(mine, part, &sum);
+    uint32_t at_tie = tied + (before >> 16), at = done + (before & 0xFFFFu) + min(at_tie, ties);
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+      const bool tie = !every && own[x] == least;
+      const bool take = every ? own[x] != 0 : own[x] > least || (tie && at_tie < ties);
+      if (tie) ++at_tie;
+      if (take) out[at++] = base + tid * kOwn + x;
+    }
+    done += sum & 0xFFFFu;
+    tied += sum >> 16;
+  }
+  for (uint32_t j = done + min(tied, ties) + tid; j < (uint32_t)sel.budget; j += kPickThreads) out[j] = -1;
 }
 
 int grid_for(int64_t n, int most) { return (int)std::min<int64_t>(std::max<int64_t>(n, 1), most); }
@@ -258,13 +380,24 @@ int launch_page_bounds(const kvtc_pages& p, const kvtc_requests& r, const int32_
   return (int)hipGetLastError();
 }
 
+template <class T>
+void launch_scores(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q, const void* bounds,
+                   const kvtc_selection& sel, uint32_t* keys, hipStream_t s) {
+  int lp = 1;
+  while (lp * 16 < p.head_dim * (int)sizeof(T)) lp *= 2;
+  // Pages per workgroup: enough workgroups to fill the GPU a few times over
+  // where there are as many pages, in whole steps of kPageThreads / lp.
+  const int64_t most = (int64_t)r.n_requests * p.kv_heads * r.table_width, step = kPageThreads / lp;
+  const int64_t span = std::min<int64_t>(16, std::max<int64_t>(1, most / (4096 * step))) * step;
+  const dim3 grid((unsigned)((r.table_width + span - 1) / span), p.kv_heads, r.n_requests);
+  hipLaunchKernelGGL(score_kernel<T>, grid, dim3(kPageThreads), 0, s, p, r, q, (const T*)bounds, sel, keys, (int)span, lp);
+}
+
 int launch_page_select(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q, const void* bounds,
                        const kvtc_selection& sel, void* ws, hipStream_t s) {
-  const dim3 grid(p.kv_heads, r.n_requests);
-  if (p.dtype == KVTC_F32)
-    hipLaunchKernelGGL(select_kernel<float>, grid, dim3(kPageThreads), 0, s, p, r, q, (const float*)bounds, sel, (uint32_t*)ws);
-  else
-    hipLaunchKernelGGL(select_kernel<uint16_t>, grid, dim3(kPageThreads), 0, s, p, r, q, (const uint16_t*)bounds, sel, (uint32_t*)ws);
+  if (p.dtype == KVTC_F32) launch_scores<float>(p, r, q, bounds, sel, (uint32_t*)ws, s);
+  else launch_scores<uint16_t>(p, r, q, bounds, sel, (uint32_t*)ws, s);
+  hipLaunchKernelGGL(pick_kernel, dim3(p.kv_heads, r.n_requests), dim3(kPickThreads), 0, s, p, r, sel, (const uint32_t*)ws);
   return (int)hipGetLastError();
 }
 
