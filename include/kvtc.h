@@ -460,8 +460,9 @@ kvtc_status kvtc_lossless_sizes(const void* d_ws, int32_t n_jobs, uint64_t* size
  * there, one without leaves its word as it was.
  *
  * Pages of KVTC_BF16 or KVTC_F32; any block_size; head_dim a multiple of 8
- * up to KVTC_MAX_HEAD_DIM; n_blocks * block_size < 2^31; at most
- * KVTC_MAX_JOBS requests per call. Page, bounds, q and out pointers are
+ * up to KVTC_MAX_HEAD_DIM; fewer than 2^31 rows in the pages, tokens in a
+ * table row and entries in all table rows; at most KVTC_MAX_JOBS requests per
+ * call. Requests may share pages. Page, bounds, q and out pointers are
  * 16-byte aligned, strides count elements and are multiples of 8.
  * ---------------------------------------------------------------------- */
 
@@ -567,7 +568,8 @@ kvtc_status kvtc_page_write(const kvtc_pages* pages, const kvtc_page_rows* rows,
  * i (from_lens NULL: all its pages; a value below 0 is read as 0):
  * bounds[page] = the smallest, then the largest value of each of the F
  * features over the page's rows below lens[i], [n_blocks, 2, F] in the pages'
- * type; bounds of other pages stay as they are. A NaN among the rows makes
+ * type; bounds of other pages stay as they are, and a page that requests share
+ * has to hold as many of each one's tokens. A NaN among the rows makes
  * both NaN. bounds_capacity: bytes at bounds. pages->v may be NULL here. */
 kvtc_status kvtc_page_bounds(const kvtc_pages* pages, const kvtc_requests* requests,
                              const int32_t* from_lens, void* bounds, size_t bounds_capacity,

@@ -157,9 +157,10 @@ def _check(status: int):
 def _ptr(x) -> int:
     if x is None:
         return 0
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
-    return int(x)
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return int(x)
 
 
 def _stream(s) -> int:

@@ -8,132 +8,268 @@ namespace {
 
 // ------------------------------------------------- block tables, slot maps ---
 
-// Each workgroup scans the requests' growth (tokens) and need (pages) into
-// LDS, which is cheaper than a launch before it, and then fills its share of
-// the table entries and slots, each found by a binary search in the scans.
+// Every workgroup scans the requests' growth in tokens and pages itself (a few
+// loads and one scan; a launch before this one would cost more) and keeps
+// them in LDS; then it fills its share of the table entries and, kSlotRun at a
+// time, of the slots, each found by one binary search in the scans.
+constexpr int kSlotRun = 4;
+__host__ __device__ constexpr size_t tables_lds_bytes(int n) { return (size_t)n * 16; }
+
 __global__ void __launch_bounds__(kPageThreads) tables_kernel(kvtc_page_plan a) {
-  extern __shared__ uint32_t lds[];
+  extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   __shared__ uint64_t part[kPageThreads / 64];
+  __shared__ uint32_t taken;
+  const int n = a.n_requests, bs = a.block_size, tid = threadIdx.x;
   uint32_t* start = lds;                       // first token of each request
-  uint32_t* page = lds + a.n_requests;         // first page of each request, behind free_from
-  const int bs = a.block_size;
-  const int64_t from = a.free_from ? max(a.free_from[0], 0) : 0;
+  uint32_t* page = lds + n;                    // first page of each request, behind free_from
+  int32_t* olds = (int32_t*)lds + 2 * n;       // tokens before; of a request that is refused -1
+  uint32_t* had = lds + 3 * n;                 // pages before
+  const uint32_t from = a.free_from ? (uint32_t)max(a.free_from[0], 0) : 0u;
   const uint64_t kCap = 0xFFFFFFFFull;         // past every n_slots and n_free
-  uint64_t tokens = 0, needed = 0, taken = 0;
-  for (int base = 0; base < a.n_requests; base += kPageThreads) {
-    const int i = base + (int)threadIdx.x;
-    int old = 0, now = 0;
-    bool ok = false;
-    if (i < a.n_requests) {
-      old = a.old_lens ? a.old_lens[i] : 0;
-      now = a.new_lens[i];
-      ok = old >= 0 && now >= old && now <= a.table_width * bs;
-    }
-    const uint64_t grow = ok ? now - old : 0;
-    const uint64_t need = ok ? pages_of(now, bs) - pages_of(old, bs) : 0;
-    uint64_t sum_t, sum_p, sum_g;
-    const uint64_t t0 = tokens + scan_threads(grow, part, &sum_t);
-    const uint64_t p0 = needed + scan_threads(need, part, &sum_p);
-    const bool fits = t0 + grow <= (uint64_t)a.n_slots && (need == 0 || from + p0 + need <= (uint64_t)a.n_free);
-    scan_threads(ok && fits ? need : (uint64_t)0, part, &sum_g);
-    if (i < a.n_requests) {
-      start[i] = (uint32_t)min(t0, kCap);
-      page[i] = (uint32_t)min(p0, kCap);
-      if (blockIdx.x == 0) {
-        if (a.starts) a.starts[i] = (int32_t)min(t0, (uint64_t)INT32_MAX);
-        if (!ok) set_status(a.status, i, KVTC_E_INVALID);
-        else if (!fits) set_status(a.status, i, KVTC_E_CAPACITY);
-      }
-    }
-    tokens += sum_t;
-    needed += sum_p;
-    taken += sum_g;
+  if (tid == 0) taken = 0;
+  const int each = (n + kPageThreads - 1) / kPageThreads, i0 = tid * each, i1 = min(i0 + each, n);
+  uint64_t tokens = 0, pages = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int old = a.old_lens ? a.old_lens[i] : 0, now = a.new_lens[i];
+    const bool ok = old >= 0 && now >= old && now <= a.table_width * bs;
+    const int before = ok ? pages_of(old, bs) : 0;
+    const uint32_t grow = ok ? now - old : 0, need = ok ? pages_of(now, bs) - before : 0;
+    olds[i] = ok ? old : -1;
+    had[i] = before;
+    start[i] = grow;
+    page[i] = need;
+    tokens += grow;
+    pages += need;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    if (a.starts) a.starts[a.n_requests] = (int32_t)min(tokens, (uint64_t)INT32_MAX);
-    if (a.taken) *a.taken = (int32_t)taken;
+  uint64_t total, total_pages;
+  uint64_t t = scan_threads(tokens, part, &total), b = scan_threads(pages, part, &total_pages);
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t grow = start[i], need = page[i];
+    const bool ok = olds[i] >= 0;
+    const bool fits = t + grow <= (uint64_t)a.n_slots && (need == 0 || from + b + need <= (uint64_t)a.n_free);
+    if (ok && fits && need) atomicMax(&taken, (uint32_t)(b + need));   // those served are the first that need pages
+    start[i] = (uint32_t)min(t, kCap);
+    page[i] = (uint32_t)min(b, kCap);
+    if (!ok || !fits) {
+      olds[i] = -1;
+      if (blockIdx.x == 0) set_status(a.status, i, ok ? KVTC_E_CAPACITY : KVTC_E_INVALID);
+    }
+    if (a.starts && blockIdx.x == 0) a.starts[i] = (int32_t)min(t, (uint64_t)INT32_MAX);
+    t += grow;
+    b += need;
   }
   __syncthreads();
-  const uint32_t stride = gridDim.x * kPageThreads, me = blockIdx.x * kPageThreads + threadIdx.x;
-  // pages given out: requests are served in order, so they are the first `taken` needed ones
-  for (uint64_t e = me; e < taken; e += stride) {
-    const int i = owner_of(page, a.n_requests, (uint32_t)e);
-    const int at = pages_of(a.old_lens ? a.old_lens[i] : 0, bs) + (int)((uint32_t)e - page[i]);
-    a.block_table[(size_t)i * a.table_stride + at] = a.free_blocks[from + e];
+  if (blockIdx.x == 0 && tid == 0) {
+    if (a.starts) a.starts[n] = (int32_t)min(total, (uint64_t)INT32_MAX);
+    if (a.taken) *a.taken = (int32_t)taken;
   }
-  for (uint64_t t = me; t < (uint64_t)a.n_slots; t += stride) {
-    int slot = -1;
-    if (t < tokens) {
-      const int i = owner_of(start, a.n_requests, (uint32_t)t);
-      const int old = a.old_lens ? a.old_lens[i] : 0, now = a.new_lens[i];
-      const int p = old + (int)((uint32_t)t - start[i]), at = p / bs, had = pages_of(old, bs);
-      const uint32_t need = pages_of(now, bs) - had;
-      const bool fits = (uint64_t)start[i] + (now - old) <= (uint64_t)a.n_slots &&
-                        (need == 0 || from + (uint64_t)page[i] + need <= (uint64_t)a.n_free);
-      if (fits) {
-        const int id = at < had ? a.block_table[(size_t)i * a.table_stride + at]
-                                : a.free_blocks[from + page[i] + (at - had)];
-        if (id >= 0 && id < a.n_blocks) slot = id * bs + p % bs;
-        else set_status(a.status, i, KVTC_E_INVALID);
+  const uint32_t stride = gridDim.x * kPageThreads, me = blockIdx.x * kPageThreads + tid;
+  for (uint32_t e = me; e < taken; e += stride) {
+    const int i = owner_of(page, n, e);
+    a.block_table[(size_t)i * a.table_stride + had[i] + (e - page[i])] = a.free_blocks[from + e];
+  }
+  const bool whole = ((uintptr_t)a.slots & 15) == 0;
+  for (uint64_t s0 = (uint64_t)me * kSlotRun; s0 < (uint64_t)a.n_slots; s0 += (uint64_t)stride * kSlotRun) {
+    int slot[kSlotRun];
+    // the request, its token and the page of the slot before
+    int i = s0 < total ? owner_of(start, n, (uint32_t)s0) : 0;
+    int at = -1, id = -1;
+#pragma unroll
+    for (int x = 0; x < kSlotRun; ++x) {
+      const uint64_t s = s0 + x;
+      slot[x] = -1;
+      if (s >= total) continue;
+      while (i + 1 < n && start[i + 1] <= s) {
+        ++i;
+        at = -1;
       }
+      if (olds[i] < 0) continue;
+      const int p = olds[i] + (int)((uint32_t)s - start[i]), j = p / bs;
+      if (j != at) {
+        at = j;
+        id = (uint32_t)j < had[i] ? a.block_table[(size_t)i * a.table_stride + j] : a.free_blocks[from + page[i] + (j - had[i])];
+        if (id < 0 || id >= a.n_blocks) {
+          id = -1;
+          set_status(a.status, i, KVTC_E_INVALID);
+        }
+      }
+      if (id >= 0) slot[x] = id * bs + p % bs;
     }
-    a.slots[t] = slot;
+    if (whole && s0 + kSlotRun <= (uint64_t)a.n_slots) {
+      *(int4*)(a.slots + s0) = int4{slot[0], slot[1], slot[2], slot[3]};
+    } else {
+#pragma unroll
+      for (int x = 0; x < kSlotRun; ++x)
+        if (s0 + x < (uint64_t)a.n_slots) a.slots[s0 + x] = slot[x];
+    }
   }
 }
 
 // ------------------------------------------------------------ write of rows ---
 
+// 8 elements in fp32 or as stored, and back.
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8), aligned(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+template <class S> struct Row8;
+template <> struct Row8<float> { typedef u32x8 type; };
+template <> struct Row8<uint16_t> { typedef u32x4 type; };
+
 template <class S, class D>
+__device__ __forceinline__ typename Row8<D>::type convert8(typename Row8<S>::type x) {
+  if constexpr (sizeof(S) == sizeof(D)) {
+    return x;
+  } else if constexpr (sizeof(S) == 4) {
+    const f32x8 f = __builtin_bit_cast(f32x8, x);
+    bf16x8 b;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = (__bf16)f[e];
+    return __builtin_bit_cast(u32x4, b);
+  } else {
+    u32x8 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r[2 * e] = x[e] << 16;
+      r[2 * e + 1] = x[e] & 0xFFFF0000u;
+    }
+    return r;
+  }
+}
+
+// A wave takes a row of K and V, 8 elements a lane at a time. A copy: bounded
+// by HBM (or, for a step's few rows, by one load after another: the rows are
+// read before their slot is known). WHOLE: rows can be read in 16-byte pieces.
+template <class S, class D, bool WHOLE>
 __global__ void __launch_bounds__(kPageThreads) write_kernel(kvtc_pages p, kvtc_page_rows r) {
-  const int F = p.kv_heads * p.head_dim;
+  typedef typename Row8<S>::type src8;
+  typedef typename Row8<D>::type dst8;
+  const int F = p.kv_heads * p.head_dim, lane = threadIdx.x & 63;
   const int64_t rows = (int64_t)p.n_blocks * p.block_size;
-  for (int64_t i = blockIdx.x; i < r.n_rows; i += gridDim.x) {
+  const int64_t first = blockIdx.x * (kPageThreads / 64) + (threadIdx.x >> 6), step = (int64_t)gridDim.x * (kPageThreads / 64);
+  for (int64_t i = first; i < r.n_rows; i += step) {
     const int64_t slot = r.slots[i];
-    if (slot >= rows && threadIdx.x == 0) set_status(r.status, 0, KVTC_E_INVALID);
-    if (slot < 0 || slot >= rows) continue;
     const S* ks = (const S*)r.k + i * r.k_stride;
     const S* vs = (const S*)r.v + i * r.v_stride;
-    D* kd = (D*)p.k + slot * F;
-    D* vd = (D*)p.v + slot * F;
-    for (int f = threadIdx.x; f < F; f += kPageThreads) {
-      Elem<D>::put(kd + f, Elem<S>::get(ks + f));
-      Elem<D>::put(vd + f, Elem<S>::get(vs + f));
+    const bool there = slot >= 0 && slot < rows;
+    if (slot >= rows && lane == 0) set_status(r.status, 0, KVTC_E_INVALID);
+    D* kd = (D*)p.k + (there ? slot : 0) * F;
+    D* vd = (D*)p.v + (there ? slot : 0) * F;
+    if constexpr (WHOLE) {
+      for (int f = 8 * lane; f < F; f += 1024) {
+        const bool two = f + 512 < F;
+        src8 a[2], b[2];
+        a[0] = *(const src8*)(ks + f);
+        b[0] = *(const src8*)(vs + f);
+        if (two) {
+          a[1] = *(const src8*)(ks + f + 512);
+          b[1] = *(const src8*)(vs + f + 512);
+        }
+        if (!there) continue;
+        *(dst8*)(kd + f) = convert8<S, D>(a[0]);
+        *(dst8*)(vd + f) = convert8<S, D>(b[0]);
+        if (two) {
+          *(dst8*)(kd + f + 512) = convert8<S, D>(a[1]);
+          *(dst8*)(vd + f + 512) = convert8<S, D>(b[1]);
+        }
+      }
+    } else if (there) {
+      for (int f = lane; f < F; f += 64) {
+        Elem<D>::put(kd + f, Elem<S>::get(ks + f));
+        Elem<D>::put(vd + f, Elem<S>::get(vs + f));
+      }
     }
   }
 }
 
 // -------------------------------------------------------------- key bounds ---
 
+// A wave takes one page's rows over 1 KB of their columns, 16 bytes a lane,
+// with the three-operand minimum and maximum that pass a NaN on (an ordinary
+// one would drop it). One pass over the keys: HBM bounds a whole cache, the
+// scan and two loads in a row a step's last pages. The page list follows from
+// the lengths: every workgroup scans them, as in tables_kernel.
+constexpr int kBoundRows = 8;      // rows in flight per lane
+
+template <class T>
+__device__ __forceinline__ void widen(u32x4 x, float* f) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(x[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(x[e] << 16);
+      f[2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u);
+    }
+  }
+}
+template <class T>
+__device__ __forceinline__ u32x4 narrow(const float* f) {      // values that T holds
+  u32x4 x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    x[e] = sizeof(T) == 4 ? __float_as_uint(f[e]) : (__float_as_uint(f[2 * e]) >> 16) | (__float_as_uint(f[2 * e + 1]) & 0xFFFF0000u);
+  return x;
+}
+
 template <class T>
 __global__ void __launch_bounds__(kPageThreads) bounds_kernel(kvtc_pages p, kvtc_requests r, const int32_t* from, T* bounds) {
-  const int i = blockIdx.y, bs = p.block_size, F = p.kv_heads * p.head_dim;
-  const int len = checked_len(r, bs, i);
-  if (len < 0) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
-    return;
+  constexpr int EL = 16 / sizeof(T);
+  extern __shared__ uint32_t first[];          // pages of the requests before each one
+  __shared__ uint32_t part[kPageThreads / 64];
+  const int n = r.n_requests, bs = p.block_size, F = p.kv_heads * p.head_dim, tid = threadIdx.x, lane = tid & 63;
+  auto since = [&](int i) { return from ? max(from[i], 0) / bs : 0; };
+  const int each = (n + kPageThreads - 1) / kPageThreads, i0 = tid * each, i1 = min(i0 + each, n);
+  uint32_t mine = 0, total;
+  for (int i = i0; i < i1; ++i) {
+    const int len = checked_len(r, bs, i);
+    if (len < 0 && blockIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
+    const uint32_t pages = max(pages_of(len, bs) - since(i), 0);
+    first[i] = pages;
+    mine += pages;
   }
-  const int a = from ? max(from[i], 0) / bs : 0;
-  for (int64_t j = a + (int64_t)blockIdx.x; j * bs < len; j += gridDim.x) {
+  uint32_t before = scan_threads(mine, part, &total);
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t pages = first[i];
+    first[i] = before;
+    before += pages;
+  }
+  __syncthreads();
+  const int slabs = (F + 64 * EL - 1) / (64 * EL);
+  const uint64_t units = (uint64_t)total * slabs, step = (uint64_t)gridDim.x * (kPageThreads / 64);
+  for (uint64_t u = (uint64_t)blockIdx.x * (kPageThreads / 64) + (tid >> 6); u < units; u += step) {
+    const uint32_t e = (uint32_t)(u / slabs);
+    const int f = ((int)(u % slabs) * 64 + lane) * EL;
+    const int i = owner_of(first, n, e), j = since(i) + (int)(e - first[i]);
     const int id = r.block_table[(int64_t)i * r.table_stride + j];
     if (id < 0 || id >= p.n_blocks) {
-      if (threadIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
+      if (lane == 0) set_status(r.status, i, KVTC_E_INVALID);
       continue;
     }
-    const int rows = min((int64_t)bs, len - j * bs);
-    for (int f = threadIdx.x; f < F; f += kPageThreads) {
-      const T* k = (const T*)p.k + (int64_t)id * bs * F + f;
-      float lo = Elem<T>::get(k), hi = lo;
-      bool nan = lo != lo;
-      for (int t = 1; t < rows; ++t) {
-        const float x = Elem<T>::get(k + (int64_t)t * F);
-        nan |= x != x;
-        lo = fminf(lo, x);
-        hi = fmaxf(hi, x);
+    if (f >= F) continue;
+    const int rows = min(bs, r.lens[i] - j * bs);
+    const T* k = (const T*)p.k + (int64_t)id * bs * F + f;
+    float lo[EL], hi[EL];
+    widen<T>(*(const u32x4*)k, lo);
+#pragma unroll
+    for (int x = 0; x < EL; ++x) hi[x] = lo[x];
+    for (int t = 0; t < rows; t += kBoundRows) {
+      u32x4 x[kBoundRows];
+#pragma unroll
+      for (int c = 0; c < kBoundRows; ++c) x[c] = *(const u32x4*)(k + (int64_t)min(t + c, rows - 1) * F);   // the last row again past the end
+#pragma unroll
+      for (int c = 0; c < kBoundRows; ++c) {
+        float v[EL];
+        widen<T>(x[c], v);
+#pragma unroll
+        for (int y = 0; y < EL; ++y) {
+          lo[y] = __builtin_elementwise_minimum(lo[y], v[y]);
+          hi[y] = __builtin_elementwise_maximum(hi[y], v[y]);
+        }
       }
-      if (nan) lo = hi = __uint_as_float(0x7FC00000u);
-      Elem<T>::put(bounds + ((int64_t)id * 2) * F + f, lo);
-      Elem<T>::put(bounds + ((int64_t)id * 2 + 1) * F + f, hi);
     }
+    T* b = bounds + (int64_t)id * 2 * F + f;
+    *(u32x4*)b = narrow<T>(lo);
+    *(u32x4*)(b + F) = narrow<T>(hi);
   }
 }
 
@@ -352,31 +488,36 @@ int grid_for(int64_t n, int most) { return (int)std::min<int64_t>(std::max<int64
 }  // namespace
 
 int launch_page_tables(const kvtc_page_plan& a, hipStream_t s) {
-  const size_t lds = (size_t)a.n_requests * 8;
-  const int grid = grid_for(((int64_t)a.n_slots + 4 * kPageThreads - 1) / (4 * kPageThreads), 1024);
+  const int64_t runs = ((int64_t)a.n_slots + kSlotRun - 1) / kSlotRun;
+  const int grid = grid_for((runs + kPageThreads - 1) / kPageThreads, 1024);
+  const size_t lds = tables_lds_bytes(a.n_requests);
+  allow_lds(tables_kernel, lds + 256);     // with what the kernel declares itself
   hipLaunchKernelGGL(tables_kernel, dim3(grid), dim3(kPageThreads), lds, s, a);
   return (int)hipGetLastError();
 }
 
-int launch_page_write(const kvtc_pages& p, const kvtc_page_rows& r, hipStream_t s) {
-  const int grid = grid_for(r.n_rows, 4096);
-  if (p.dtype == KVTC_F32 && r.dtype == KVTC_F32)
-    hipLaunchKernelGGL((write_kernel<float, float>), dim3(grid), dim3(kPageThreads), 0, s, p, r);
-  else if (p.dtype == KVTC_F32)
-    hipLaunchKernelGGL((write_kernel<uint16_t, float>), dim3(grid), dim3(kPageThreads), 0, s, p, r);
-  else if (r.dtype == KVTC_F32)
-    hipLaunchKernelGGL((write_kernel<float, uint16_t>), dim3(grid), dim3(kPageThreads), 0, s, p, r);
-  else
-    hipLaunchKernelGGL((write_kernel<uint16_t, uint16_t>), dim3(grid), dim3(kPageThreads), 0, s, p, r);
+template <class S, class D>
+int launch_write(const kvtc_pages& p, const kvtc_page_rows& r, hipStream_t s) {
+  const int grid = grid_for(((int64_t)r.n_rows + kPageThreads / 64 - 1) / (kPageThreads / 64), 1 << 14);
+  const bool whole = (((uintptr_t)r.k | (uintptr_t)r.v) & 15) == 0 && (r.k_stride | r.v_stride) % (int64_t)(16 / sizeof(S)) == 0;
+  if (whole) hipLaunchKernelGGL((write_kernel<S, D, true>), dim3(grid), dim3(kPageThreads), 0, s, p, r);
+  else hipLaunchKernelGGL((write_kernel<S, D, false>), dim3(grid), dim3(kPageThreads), 0, s, p, r);
   return (int)hipGetLastError();
 }
 
+int launch_page_write(const kvtc_pages& p, const kvtc_page_rows& r, hipStream_t s) {
+  if (p.dtype == KVTC_F32) return r.dtype == KVTC_F32 ? launch_write<float, float>(p, r, s) : launch_write<uint16_t, float>(p, r, s);
+  return r.dtype == KVTC_F32 ? launch_write<float, uint16_t>(p, r, s) : launch_write<uint16_t, uint16_t>(p, r, s);
+}
+
 int launch_page_bounds(const kvtc_pages& p, const kvtc_requests& r, const int32_t* from, void* bounds, hipStream_t s) {
-  const dim3 grid(grid_for(r.table_width, std::max(1, 8192 / r.n_requests)), r.n_requests);
+  const int64_t slabs = ((int64_t)p.kv_heads * p.head_dim * (p.dtype == KVTC_F32 ? 4 : 2) + 1023) / 1024;
+  const int grid = grid_for((int64_t)r.n_requests * r.table_width * slabs / (kPageThreads / 64) + 1, 2048);
+  const size_t lds = (size_t)r.n_requests * 4;
   if (p.dtype == KVTC_F32)
-    hipLaunchKernelGGL(bounds_kernel<float>, grid, dim3(kPageThreads), 0, s, p, r, from, (float*)bounds);
+    hipLaunchKernelGGL(bounds_kernel<float>, dim3(grid), dim3(kPageThreads), lds, s, p, r, from, (float*)bounds);
   else
-    hipLaunchKernelGGL(bounds_kernel<uint16_t>, grid, dim3(kPageThreads), 0, s, p, r, from, (uint16_t*)bounds);
+    hipLaunchKernelGGL(bounds_kernel<uint16_t>, dim3(grid), dim3(kPageThreads), lds, s, p, r, from, (uint16_t*)bounds);
   return (int)hipGetLastError();
 }
 

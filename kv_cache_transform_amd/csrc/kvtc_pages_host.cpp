@@ -71,8 +71,9 @@ kvtc_status check_requests(const kvtc_requests* r, const kvtc_pages& p, bool dat
   if (st != KVTC_OK) return st;
   if (r->table_width <= 0 || r->table_stride < r->table_width)
     return report(KVTC_E_INVALID, "requests: bad table_width or table_stride");
-  if ((int64_t)r->table_width * p.block_size > (int64_t)INT32_MAX)
-    return report(KVTC_E_UNSUPPORTED, "requests: tables of 2^31 tokens or more");
+  if ((int64_t)r->table_width * p.block_size > (int64_t)INT32_MAX ||
+      (int64_t)r->table_width * r->n_requests > (int64_t)INT32_MAX)
+    return report(KVTC_E_UNSUPPORTED, "requests: a table row of 2^31 tokens, or 2^31 table entries, or more");
   if (!data) return KVTC_OK;
   if (!r->block_table || !r->lens || !aligned4(r->block_table) || !aligned4(r->lens) || !aligned4(r->status))
     return report(KVTC_E_INVALID, "requests: block_table and lens must be non-null, all 4-byte aligned");

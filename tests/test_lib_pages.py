@@ -59,7 +59,7 @@ BAD_PAGES = [
 BAD_REQUESTS = [
     (INV, dict(block_table=0)), (INV, dict(lens=0)), (INV, dict(lens=P + 2)), (INV, dict(n_requests=0)), (INV, dict(n_requests=-1)),
     (CAP, dict(n_requests=K.KVTC_MAX_JOBS + 1)), (INV, dict(table_width=0)), (INV, dict(table_stride=3)),
-    (UNS, dict(table_width=1 << 27)), (INV, dict(status=P + 1)),
+    (UNS, dict(table_width=1 << 27)), (UNS, dict(table_width=1 << 20, n_requests=1 << 12)), (INV, dict(status=P + 1)),
 ]
 
 
