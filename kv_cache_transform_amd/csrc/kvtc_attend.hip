@@ -68,8 +68,8 @@ struct Tile<uint16_t, DP> {
   // the head's elements of the lane's key rows and value rows
   static constexpr int KR = 2;
   __device__ __forceinline__ static int key_at(int t, int r) { return 4 * t + (r & 3); }   // of its group
-  template <class KP, class VP>
-  __device__ __forceinline__ void load(KP kp, VP vp, int D, int g, int r) {
+  template <class KP>
+  __device__ __forceinline__ void load_keys(KP kp, int D, int g) {
 #pragma unroll
     for (int t = 0; t < KR; ++t)
 #pragma unroll
@@ -77,6 +77,9 @@ struct Tile<uint16_t, DP> {
         const int d = 32 * s + 8 * g;
         k[t][s] = *(const u32x4*)(kp(t) + (d < D ? d : 0));
       }
+  }
+  template <class VP>
+  __device__ __forceinline__ void load_values(VP vp, int D, int r) {
 #pragma unroll
     for (int e = 0; e < TG; ++e)
 #pragma unroll
@@ -160,13 +163,16 @@ struct Tile<float, DP> {
   f32x4 v[TG][VB];
   static constexpr int KR = 1;
   __device__ __forceinline__ static int key_at(int, int r) { return r & 3; }
-  template <class KP, class VP>
-  __device__ __forceinline__ void load(KP kp, VP vp, int D, int g, int r) {
+  template <class KP>
+  __device__ __forceinline__ void load_keys(KP kp, int D, int g) {
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int d = 16 * s + 4 * g;
       k[s] = *(const f32x4*)(kp(0) + (d < D ? d : 0));
     }
+  }
+  template <class VP>
+  __device__ __forceinline__ void load_values(VP vp, int D, int r) {
 #pragma unroll
     for (int e = 0; e < TG; ++e)
 #pragma unroll
@@ -230,56 +236,69 @@ __device__ __forceinline__ float sum_groups(float x) {
   return x + __shfl_xor(x, 32, 64);
 }
 
-// A position's row in the pages, and whether it is attended to (bit 0); for
-// whole groups of positions the first one's row and a bit for each.
-struct Place {
-  int64_t row;
+// One lane's lookups of a tile: the rows of its key group and value group, or
+// with pages that cut groups of each row of them, and which positions of the
+// value group (the score group too) are attended to.
+template <class TT, bool GROUPED>
+struct Places {
+  int32_t k[GROUPED ? 1 : TT::KR], v[GROUPED ? 1 : TT::TG];
   uint32_t live;
 };
 
 // DP: head_dim rounded up to 64, 128 or 256. GROUPED: every page holds whole
 // groups of TG positions (block_size is a multiple), so a lane looks up two
 // pages a tile and not one for each of its rows.
+//
+// The next tile's keys are loaded into the registers of this one's as soon as
+// the scores are computed, its values after the second product; the pages of
+// the one after are looked up before them, so that no wait for a lookup waits
+// for data behind it. One set of registers leaves room for more waves.
 template <class T, int DP, bool GROUPED>
 __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(AttendArgs a) {
   typedef Tile<T, DP> TT;
+  typedef Places<TT, GROUPED> PL;
   constexpr int TK = TT::TK, TG = TT::TG, CH = NW * TK, NS = TK / 4;
+  constexpr uint32_t kFull = (1u << TG) - 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ uint32_t scan_part[NW];
   __shared__ float wm[NW][16], wl[NW][16];
   float* wo = (float*)lds;                                              // [NW][gt][DP]
   uint32_t* pre = (uint32_t*)(lds + (size_t)NW * a.gt * DP * 4);        // chunks of the requests before each one, per row
+  int32_t* lens = (int32_t*)pre + a.r.n_requests;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
   const int n_req = a.r.n_requests, bs = a.p.block_size, D = a.p.head_dim, rows_each = a.p.kv_heads * a.tiles;
   const int64_t F = (int64_t)a.p.kv_heads * D;
 
-  // positions of request i: its tokens, or those of as many selected pages as it has pages
-  auto positions = [&](int len) -> int {
-    if (!a.sel.blocks) return max(len, 0);
-    return min(a.sel.budget, pages_of(len, bs)) * bs;
-  };
+  // positions of a request: its tokens, or those of as many selected pages as it has pages
+  auto positions = [&](int len) -> int { return a.sel.blocks ? min(a.sel.budget, pages_of(len, a.div)) * bs : len; };
   uint32_t total;
   {
-    const int each = (n_req + kPageThreads - 1) / kPageThreads, i0 = threadIdx.x * each;
-    uint32_t mine = 0;
-    for (int i = i0; i < min(i0 + each, n_req); ++i) {
-      const int len = checked_len(a.r, bs, i);
-      if (len < 0 && blockIdx.x == 0) set_status(a.r.status, i, KVTC_E_INVALID);
-      mine += (uint32_t)((positions(len) + CH - 1) / CH);
+    const int each = (n_req + kPageThreads - 1) / kPageThreads, i0 = threadIdx.x * each, i1 = min(i0 + each, n_req);
+    uint32_t scan[1] = {0}, sum[1];
+    for (int i = i0; i < i1; ++i) {
+      int len = checked_len(a.r, bs, i);
+      if (len < 0) {
+        if (blockIdx.x == 0) set_status(a.r.status, i, KVTC_E_INVALID);
+        len = 0;
+      }
+      lens[i] = len;
+      pre[i] = (uint32_t)((positions(len) + CH - 1) / CH);
+      scan[0] += pre[i];
     }
-    uint32_t before = scan_threads(mine, scan_part, &total);
-    for (int i = i0; i < min(i0 + each, n_req); ++i) {
-      pre[i] = before;
-      before += (uint32_t)((positions(checked_len(a.r, bs, i)) + CH - 1) / CH);
+    scan_threads<NW>(scan, scan_part, sum);
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t n = pre[i];
+      pre[i] = scan[0];
+      scan[0] += n;
     }
+    total = sum[0] * rows_each;
   }
   __syncthreads();
-  total *= rows_each;
   const uint32_t per = (total + gridDim.x - 1) / gridDim.x;
   const uint32_t u0 = min(blockIdx.x * per, total), u1 = min(u0 + per, total);
   // requests without a token have no chunk
   for (int i = blockIdx.x * NW + wave; i < n_req; i += gridDim.x * NW)
-    if (checked_len(a.r, bs, i) <= 0) {
+    if (lens[i] == 0) {
       for (int d = lane; d < a.q.q_heads * D; d += 64) Elem<T>::put((T*)a.q.out + i * a.q.out_stride + d, 0.0f);
       for (int h = lane; a.q.lse && h < a.q.q_heads; h += 64) a.q.lse[(int64_t)i * a.q.q_heads + h] = -INFINITY;
     }
@@ -288,8 +307,7 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
   for (uint32_t u = u0; u < u1;) {
     // the row: request i, KV head h, query tile qt; its chunks [c0, c1) of n
     const int i = owner_of(pre, n_req, u / rows_each);
-    const int len = checked_len(a.r, bs, i);
-    const int n_pos = positions(len), n_pages = pages_of(len, bs);
+    const int len = lens[i], n_pos = positions(len), n_pages = pages_of(len, a.div);
     const uint32_t n = (uint32_t)((n_pos + CH - 1) / CH), at = u - pre[i] * rows_each, row = at / n;
     const int h = (int)row / a.tiles, qt = (int)row % a.tiles;
     const uint32_t c0 = at - row * n, c1 = min(n, c0 + (u1 - u));
@@ -297,79 +315,108 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
     const int32_t* list = a.sel.blocks ? a.sel.blocks + ((int64_t)i * a.p.kv_heads + h) * a.sel.budget : nullptr;
     const int32_t* table = a.r.block_table + (int64_t)i * a.r.table_stride;
     const int64_t q_at = ((int64_t)h * a.group + 16 * qt) * D;
-    typename TT::Query q;
-    q.load((const T*)a.q.q + i * a.q.q_stride + q_at + (int64_t)r * D, D, g, r < nq);
-    const float c = a.q.scale * kLog2e;
-    float m = -INFINITY, l = 0.0f;
-    f32x4 o[TT::OUT];
-#pragma unroll
-    for (int j = 0; j < TT::OUT; ++j) o[j] = f32x4{0, 0, 0, 0};
+    const T* kh = (const T*)a.p.k + h * D;
+    const T* vh = (const T*)a.p.v + h * D;
 
-    auto place = [&](int pos) -> Place {
-      Place w = {0, 0};
-      if (pos >= n_pos) return w;
+    // the row of a position (the first of its group) and how many tokens lie from there on, 0 for none
+    auto place = [&](int pos, int32_t* row_at) -> int {
+      *row_at = 0;
+      if (pos >= n_pos) return 0;
       const uint32_t slot = div_block(pos, a.div);
       const int off = pos - (int)slot * bs;
       const int j = list ? list[slot] : (int)slot;
-      if (j < 0 || j >= n_pages) return w;
+      if (j < 0 || j >= n_pages) return 0;
       const int id = table[j];
       if (id < 0 || id >= a.p.n_blocks) {
         set_status(a.r.status, i, KVTC_E_INVALID);
-        return w;
+        return 0;
       }
-      w.row = (int64_t)id * bs + off;
-      const int left = len - (j * bs + off);       // tokens from here on
-      if (GROUPED) w.live = left >= TG ? (1u << TG) - 1 : left > 0 ? (1u << left) - 1 : 0u;
-      else w.live = left > 0;
+      *row_at = id * bs + off;
+      return max(len - (j * bs + off), 0);
+    };
+    auto look_up = [&](uint32_t ch) -> PL {
+      const int P = (int)ch * CH + wave * TK, kg = P + TG * (r >> 2), vg = P + TG * g;
+      PL w;
+      if constexpr (GROUPED) {
+        (void)place(kg, &w.k[0]);
+        const int left = place(vg, &w.v[0]);
+        w.live = left >= TG ? kFull : (1u << left) - 1;
+      } else {
+        w.live = 0;
+#pragma unroll
+        for (int x = 0; x < TT::KR; ++x) (void)place(kg + TT::key_at(x, r), &w.k[x]);
+#pragma unroll
+        for (int e = 0; e < TG; ++e) w.live |= place(vg + e, &w.v[e]) > 0 ? 1u << e : 0u;
+      }
       return w;
     };
-    const T* kh = (const T*)a.p.k + h * D;
-    const T* vh = (const T*)a.p.v + h * D;
-    for (uint32_t ch = c0; ch < c1; ++ch) {
-      const int P = (int)ch * CH + wave * TK, kg = P + TG * (r >> 2), vg = P + TG * g;
-      TT t;
-      uint32_t live = 0;       // of the value group, which is the score group too
+    TT t;
+    auto load_keys = [&](const PL& w) {
       if constexpr (GROUPED) {
-        const Place kw = place(kg), vw = place(vg);
-        const T* kp = kh + kw.row * F;
-        const T* vp = vh + vw.row * F;
-        t.load([&](int x) { return kp + TT::key_at(x, r) * F; }, [&](int e) { return vp + e * F; }, D, g, r);
-        live = vw.live;
+        const T* kp = kh + w.k[0] * F;
+        t.load_keys([&](int x) { return kp + TT::key_at(x, r) * F; }, D, g);
       } else {
-        int64_t kr[TT::KR], vr[TG];
-#pragma unroll
-        for (int x = 0; x < TT::KR; ++x) kr[x] = place(kg + TT::key_at(x, r)).row;
-#pragma unroll
-        for (int e = 0; e < TG; ++e) {
-          const Place w = place(vg + e);
-          vr[e] = w.row;
-          live |= w.live << e;
-        }
-        t.load([&](int x) { return kh + kr[x] * F; }, [&](int e) { return vh + vr[e] * F; }, D, g, r);
+        t.load_keys([&](int x) { return kh + w.k[x] * F; }, D, g);
       }
+    };
+    auto load_values = [&](const PL& w) {
+      if constexpr (GROUPED) {
+        const T* vp = vh + w.v[0] * F;
+        t.load_values([&](int e) { return vp + e * F; }, D, r);
+      } else {
+        t.load_values([&](int e) { return vh + w.v[e] * F; }, D, r);
+      }
+    };
+    typename TT::Query q;
+    const float c = a.q.scale * kLog2e;
+    float m = -INFINITY, l = 0.0f;
+    f32x4 o[TT::OUT];
+
+    PL now = look_up(c0);
+    q.load((const T*)a.q.q + i * a.q.q_stride + q_at + (int64_t)r * D, D, g, r < nq);
+#pragma unroll
+    for (int j = 0; j < TT::OUT; ++j) o[j] = f32x4{0, 0, 0, 0};
+    PL next = look_up(c0 + 1);
+    load_keys(now);
+    load_values(now);
+    for (uint32_t ch = c0; ch < c1; ++ch) {
+      const uint32_t live = now.live;
+      const PL after = look_up(ch + 2);
       if (D != DP) t.mask_dims(D, g);
       float s[NS];
       t.scores(q, s);
-      float top = -INFINITY;
+      if (ch + 1 < c1) load_keys(next);
 #pragma unroll
-      for (int e = 0; e < NS; ++e) {
-        s[e] = live >> e & 1 ? s[e] * c : -INFINITY;
-        top = fmaxf(top, s[e]);
+      for (int e = 0; e < NS; ++e) s[e] *= c;
+      if (__any(live != kFull)) {
+#pragma unroll
+        for (int e = 0; e < NS; ++e)
+          if (!(live >> e & 1)) s[e] = -INFINITY;
+        t.mask_rows(live);
       }
-      t.mask_rows(live);
-      top = fmaxf(m, max_groups(top));
-      const float base = top == -INFINITY ? 0.0f : top;
-      const float f = __builtin_amdgcn_exp2f(m - base);
-      m = top;
-      l *= f;
+      // The maximum that the weights are taken relative to moves only when a
+      // score passes it by 2^8, far from fp32's range, so that almost no tile
+      // has to look across lanes or rescale the sums.
+      float top = s[0];
 #pragma unroll
-      for (int j = 0; j < TT::OUT; ++j) o[j] *= f;
+      for (int e = 1; e < NS; ++e) top = fmaxf(top, s[e]);
+      if (__any(top > m + 8.0f)) {
+        const float to = fmaxf(m, max_groups(top)), f = __builtin_amdgcn_exp2f(m - (to == -INFINITY ? 0.0f : to));
+        m = to;
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < TT::OUT; ++j) o[j] *= f;
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
       for (int e = 0; e < NS; ++e) {
         s[e] = __builtin_amdgcn_exp2f(s[e] - base);
         l += s[e];
       }
       t.add_values(s, o);
+      if (ch + 1 < c1) load_values(next);
+      now = next;
+      next = after;
     }
 
     // join the waves
@@ -489,8 +536,8 @@ __global__ void __launch_bounds__(kPageThreads) join_kernel(AttendArgs a) {
 
 template <class T, int DP, bool GROUPED>
 void launch_pieces(const AttendArgs& a, uint32_t grid, hipStream_t s) {
-  const size_t lds = (size_t)NW * a.gt * DP * 4 + (size_t)a.r.n_requests * 4;
-  allow_lds(attend_kernel<T, DP, GROUPED>, lds);
+  const size_t lds = (size_t)NW * a.gt * DP * 4 + (size_t)a.r.n_requests * 8;
+  allow_lds(attend_kernel<T, DP, GROUPED>, lds + 1024);      // with what the kernel declares itself
   hipLaunchKernelGGL((attend_kernel<T, DP, GROUPED>), dim3(grid), dim3(kPageThreads), lds, s, a);
 }
 

@@ -15,52 +15,53 @@ namespace {
 constexpr int kSlotRun = 4;
 __host__ __device__ constexpr size_t tables_lds_bytes(int n) { return (size_t)n * 16; }
 
-__global__ void __launch_bounds__(kPageThreads) tables_kernel(kvtc_page_plan a) {
+__global__ void __launch_bounds__(kPageThreads) tables_kernel(kvtc_page_plan a, BlockDiv div) {
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
-  __shared__ uint64_t part[kPageThreads / 64];
-  __shared__ uint32_t taken;
+  __shared__ uint32_t part[2 * kPageThreads / 64], taken;
   const int n = a.n_requests, bs = a.block_size, tid = threadIdx.x;
   uint32_t* start = lds;                       // first token of each request
   uint32_t* page = lds + n;                    // first page of each request, behind free_from
   int32_t* olds = (int32_t*)lds + 2 * n;       // tokens before; of a request that is refused -1
   uint32_t* had = lds + 3 * n;                 // pages before
   const uint32_t from = a.free_from ? (uint32_t)max(a.free_from[0], 0) : 0u;
-  const uint64_t kCap = 0xFFFFFFFFull;         // past every n_slots and n_free
   if (tid == 0) taken = 0;
   const int each = (n + kPageThreads - 1) / kPageThreads, i0 = tid * each, i1 = min(i0 + each, n);
-  uint64_t tokens = 0, pages = 0;
+  uint32_t scan[2] = {0, 0}, total[2];         // tokens, pages
   for (int i = i0; i < i1; ++i) {
     const int old = a.old_lens ? a.old_lens[i] : 0, now = a.new_lens[i];
     const bool ok = old >= 0 && now >= old && now <= a.table_width * bs;
-    const int before = ok ? pages_of(old, bs) : 0;
-    const uint32_t grow = ok ? now - old : 0, need = ok ? pages_of(now, bs) - before : 0;
+    const int before = ok ? pages_of(old, div) : 0;
+    const uint32_t grow = ok ? now - old : 0, need = ok ? pages_of(now, div) - before : 0;
     olds[i] = ok ? old : -1;
     had[i] = before;
     start[i] = grow;
     page[i] = need;
-    tokens += grow;
-    pages += need;
+    scan[0] = add_sat(scan[0], grow);
+    scan[1] = add_sat(scan[1], need);
   }
-  uint64_t total, total_pages;
-  uint64_t t = scan_threads(tokens, part, &total), b = scan_threads(pages, part, &total_pages);
+  scan_threads<kPageThreads / 64>(scan, part, total);
+  uint32_t t = scan[0], b = scan[1], most = 0;
   for (int i = i0; i < i1; ++i) {
     const uint32_t grow = start[i], need = page[i];
     const bool ok = olds[i] >= 0;
-    const bool fits = t + grow <= (uint64_t)a.n_slots && (need == 0 || from + b + need <= (uint64_t)a.n_free);
-    if (ok && fits && need) atomicMax(&taken, (uint32_t)(b + need));   // those served are the first that need pages
-    start[i] = (uint32_t)min(t, kCap);
-    page[i] = (uint32_t)min(b, kCap);
+    const bool fits = add_sat(t, grow) <= (uint32_t)a.n_slots &&
+                      (need == 0 || add_sat(from, add_sat(b, need)) <= (uint32_t)a.n_free);
+    if (ok && fits && need) most = b + need;   // those served are the first that need pages
+    start[i] = t;
+    page[i] = b;
     if (!ok || !fits) {
       olds[i] = -1;
       if (blockIdx.x == 0) set_status(a.status, i, ok ? KVTC_E_CAPACITY : KVTC_E_INVALID);
     }
-    if (a.starts && blockIdx.x == 0) a.starts[i] = (int32_t)min(t, (uint64_t)INT32_MAX);
-    t += grow;
-    b += need;
+    if (a.starts && blockIdx.x == 0) a.starts[i] = (int32_t)min(t, (uint32_t)INT32_MAX);
+    t = add_sat(t, grow);
+    b = add_sat(b, need);
   }
+  most = last_lane(wave_scan(most, 0u, [](uint32_t x, uint32_t y) { return max(x, y); }));
+  if ((tid & 63) == 0 && most) atomicMax(&taken, most);
   __syncthreads();
   if (blockIdx.x == 0 && tid == 0) {
-    if (a.starts) a.starts[n] = (int32_t)min(total, (uint64_t)INT32_MAX);
+    if (a.starts) a.starts[n] = (int32_t)min(total[0], (uint32_t)INT32_MAX);
     if (a.taken) *a.taken = (int32_t)taken;
   }
   const uint32_t stride = gridDim.x * kPageThreads, me = blockIdx.x * kPageThreads + tid;
@@ -72,19 +73,19 @@ __global__ void __launch_bounds__(kPageThreads) tables_kernel(kvtc_page_plan a) 
   for (uint64_t s0 = (uint64_t)me * kSlotRun; s0 < (uint64_t)a.n_slots; s0 += (uint64_t)stride * kSlotRun) {
     int slot[kSlotRun];
     // the request, its token and the page of the slot before
-    int i = s0 < total ? owner_of(start, n, (uint32_t)s0) : 0;
+    int i = s0 < total[0] ? owner_of(start, n, (uint32_t)s0) : 0;
     int at = -1, id = -1;
 #pragma unroll
     for (int x = 0; x < kSlotRun; ++x) {
       const uint64_t s = s0 + x;
       slot[x] = -1;
-      if (s >= total) continue;
+      if (s >= total[0]) continue;
       while (i + 1 < n && start[i + 1] <= s) {
         ++i;
         at = -1;
       }
       if (olds[i] < 0) continue;
-      const int p = olds[i] + (int)((uint32_t)s - start[i]), j = p / bs;
+      const int p = olds[i] + (int)((uint32_t)s - start[i]), j = (int)div_block(p, div);
       if (j != at) {
         at = j;
         id = (uint32_t)j < had[i] ? a.block_table[(size_t)i * a.table_stride + j] : a.free_blocks[from + page[i] + (j - had[i])];
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kPageThreads) tables_kernel(kvtc_page_plan a) 
           set_status(a.status, i, KVTC_E_INVALID);
         }
       }
-      if (id >= 0) slot[x] = id * bs + p % bs;
+      if (id >= 0) slot[x] = id * bs + (p - j * bs);
     }
     if (whole && s0 + kSlotRun <= (uint64_t)a.n_slots) {
       *(int4*)(a.slots + s0) = int4{slot[0], slot[1], slot[2], slot[3]};
@@ -212,22 +213,24 @@ __device__ __forceinline__ u32x4 narrow(const float* f) {      // values that T 
 }
 
 template <class T>
-__global__ void __launch_bounds__(kPageThreads) bounds_kernel(kvtc_pages p, kvtc_requests r, const int32_t* from, T* bounds) {
+__global__ void __launch_bounds__(kPageThreads) bounds_kernel(kvtc_pages p, kvtc_requests r, BlockDiv div, const int32_t* from, T* bounds) {
   constexpr int EL = 16 / sizeof(T);
   extern __shared__ uint32_t first[];          // pages of the requests before each one
   __shared__ uint32_t part[kPageThreads / 64];
   const int n = r.n_requests, bs = p.block_size, F = p.kv_heads * p.head_dim, tid = threadIdx.x, lane = tid & 63;
-  auto since = [&](int i) { return from ? max(from[i], 0) / bs : 0; };
+  auto since = [&](int i) { return from ? (int)div_block(max(from[i], 0), div) : 0; };
   const int each = (n + kPageThreads - 1) / kPageThreads, i0 = tid * each, i1 = min(i0 + each, n);
-  uint32_t mine = 0, total;
+  uint32_t scan[1] = {0}, sum[1];
   for (int i = i0; i < i1; ++i) {
     const int len = checked_len(r, bs, i);
     if (len < 0 && blockIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
-    const uint32_t pages = max(pages_of(len, bs) - since(i), 0);
+    const uint32_t pages = max(pages_of(len, div) - since(i), 0);
     first[i] = pages;
-    mine += pages;
+    scan[0] += pages;
   }
-  uint32_t before = scan_threads(mine, part, &total);
+  scan_threads<kPageThreads / 64>(scan, part, sum);
+  uint32_t before = scan[0];
+  const uint32_t total = sum[0];
   for (int i = i0; i < i1; ++i) {
     const uint32_t pages = first[i];
     first[i] = before;
@@ -284,6 +287,26 @@ __device__ __forceinline__ uint32_t score_key(double s) {
   return f != f ? kKeyNan : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// x + its value in the lane that CTRL names.
+template <int CTRL>
+__device__ __forceinline__ double add_moved(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint64_t v = (uint64_t)lane_move<CTRL>(0u, (uint32_t)(u >> 32)) << 32 | lane_move<CTRL>(0u, (uint32_t)u);
+  return x + __builtin_bit_cast(double, v);
+}
+// The sum over every aligned group of LP lanes (a power of two), in each lane:
+// neighbours, pairs, then the mirrored half rows and rows, whose lanes hold
+// equal sums by then, then across rows.
+__device__ __forceinline__ double sum_lanes(double x, int LP) {
+  if (LP > 1) x = add_moved<0xB1>(x);        // quad_perm 1 0 3 2
+  if (LP > 2) x = add_moved<0x4E>(x);        // quad_perm 2 3 0 1
+  if (LP > 4) x = add_moved<0x141>(x);       // row_half_mirror
+  if (LP > 8) x = add_moved<0x140>(x);       // row_mirror
+  if (LP > 16) x += __shfl_xor(x, 16, 64);
+  if (LP > 32) x += __shfl_xor(x, 32, 64);
+  return x;
+}
+
 // Scores of the pages [blockIdx.x * span, + span) of request blockIdx.z for KV
 // head blockIdx.y. LP lanes (a power of two) share a page, 16 bytes of each
 // bound to a lane, so a load instruction covers whole 16 * LP byte rows; each
@@ -292,12 +315,12 @@ __device__ __forceinline__ uint32_t score_key(double s) {
 // time that HBM takes for them.
 template <class T>
 __global__ void __launch_bounds__(kPageThreads) score_kernel(kvtc_pages p, kvtc_requests r, kvtc_queries q, const T* bounds,
-                                                             kvtc_selection sel, uint32_t* keys, int span, int LP) {
+                                                             BlockDiv div, kvtc_selection sel, uint32_t* keys, int span, int LP) {
   constexpr int EL = 16 / sizeof(T);
   typedef T row16 __attribute__((ext_vector_type(EL)));
   const int h = blockIdx.y, i = blockIdx.z, bs = p.block_size, D = p.head_dim, F = p.kv_heads * D;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d0 = (lane & (LP - 1)) * EL;
-  const int len = checked_len(r, bs, i), n = pages_of(len, bs), j0 = (int)blockIdx.x * span;
+  const int len = checked_len(r, bs, i), n = pages_of(len, div), j0 = (int)blockIdx.x * span;
   if (len < 0 && j0 == 0 && h == 0 && threadIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
   if (j0 >= n) return;
   const int j1 = min(n, j0 + span);
@@ -336,8 +359,7 @@ __global__ void __launch_bounds__(kPageThreads) score_kernel(kvtc_pages p, kvtc_
         s1 = fma(up[e], (double)Elem<T>::get(&he), s1);
       }
     }
-    s0 += s1;
-    for (int m = LP >> 1; m; m >>= 1) s0 += __shfl_xor(s0, m, 64);
+    s0 = sum_lanes(s0 + s1, LP);
     if (j < j1 && (lane & (LP - 1)) == 0) {
       key[j] = !ok ? 0u : keep ? kKeyKeep : score_key(s0);
       if (!ok) set_status(r.status, i, KVTC_E_INVALID);
@@ -354,35 +376,14 @@ __global__ void __launch_bounds__(kPageThreads) score_kernel(kvtc_pages p, kvtc_
 // kPickThreads pages; past them they are read again for every digit.
 constexpr int kPickThreads = 1024, kOwn = 8, kDigit = 11;
 
-template <class V>
-__device__ __forceinline__ V scan_picks(V v, V* part, V* sum) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  V x = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const V y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
-  }
-  __syncthreads();
-  if (lane == 63) part[wave] = x;
-  __syncthreads();
-  V before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kPickThreads / 64; ++w) {
-    const V y = part[w];
-    if (w < wave) before += y;
-    all += y;
-  }
-  *sum = all;
-  return before + x - v;
-}
-
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_requests r, kvtc_selection sel, const uint32_t* keys) {
-  __shared__ uint32_t count[1 << kDigit], part[kPickThreads / 64], found[2], range[2];
-  const int h = blockIdx.x, i = blockIdx.y, bs = p.block_size, tid = threadIdx.x;
-  const int n = pages_of(checked_len(r, bs, i), bs), span = kOwn * kPickThreads;
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_requests r, BlockDiv div, kvtc_selection sel, const uint32_t* keys) {
+  constexpr int W = kPickThreads / 64, span = kOwn * kPickThreads;
+  __shared__ uint32_t count[1 << kDigit], part[2 * W], ends[2 * W], found[3];
+  const int h = blockIdx.x, i = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = pages_of(checked_len(r, p.block_size, i), div);
   const uint32_t* key = keys + ((int64_t)i * p.kv_heads + h) * r.table_width;
   int32_t* out = sel.blocks + ((int64_t)i * p.kv_heads + h) * sel.budget;
+  const uint32_t budget = sel.budget;
   uint32_t own[kOwn];
   auto read = [&](int base) {      // this thread's keys of pages [base, base + span)
 #pragma unroll
@@ -393,83 +394,86 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_r
   };
   auto each = [&](auto f) {        // f(key) for every key of this thread
     for (int base = 0; base < n; base += span) {
-      if (base || n > span) read(base);
+      if (n > span) read(base);
 #pragma unroll
       for (int x = 0; x < kOwn; ++x) f(own[x]);
     }
   };
   read(0);
+#pragma unroll
+  for (int x = tid; x < 1 << kDigit; x += kPickThreads) count[x] = 0;
   // Only keys between those that are never taken and those that always are
   // can be the threshold; is there a choice at all?
-  if (tid < 2) range[tid] = tid ? 0u : 0xFFFFFFFFu;
-  uint32_t lo = 0xFFFFFFFFu, hi = 0u, valid = 0, kept = 0;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u, some[2] = {0, 0}, sums[2];      // valid, kept
   each([&](uint32_t k) {
-    valid += k != 0;
-    kept += k == kKeyKeep;
+    some[0] += k != 0;
+    some[1] += k == kKeyKeep;
     if (k && k != kKeyKeep) {
       lo = min(lo, k);
       hi = max(hi, k);
     }
   });
-  uint32_t n_valid, n_kept;
-  scan_picks(valid, part, &n_valid);
-  scan_picks(kept, part, &n_kept);
-  uint32_t least = 1, ties = 0;       // taken: keys above least, and the first `ties` at it
-  if (n_valid > (uint32_t)sel.budget) {
-    atomicMin(&range[0], lo);
-    atomicMax(&range[1], hi);
-    uint32_t want = sel.budget - n_kept;       // of the keys in [lo, hi], the host has seen to want >= 0
-    __syncthreads();
-    lo = range[0];
-    hi = range[1];
-    if (want == 0) {
-      least = kKeyNan;
-      ties = 0;
-    } else {
-      // the keys in question are lo + [0, 2^bits)
-      int bits = 32 - __clz((int)max(hi - lo, 1u));
-      for (;;) {
-        const int low = max(bits - kDigit, 0);
-        for (int x = tid; x < 1 << kDigit; x += kPickThreads) count[x] = 0;
-        __syncthreads();
-        const uint32_t top = hi - lo;
-        each([&](uint32_t k) {
-          if (k >= lo && k - lo <= top && k != kKeyKeep) atomicAdd(&count[(k - lo) >> low], 1u);
-        });
-        __syncthreads();
-        // from the highest digit down: thread t holds digits 2 (last - t) + 1 and 2 (last - t)
-        const int x = 2 * (kPickThreads - 1 - tid);
-        const uint32_t b = count[x + 1], a = count[x];
-        uint32_t sum;
-        const uint32_t above = scan_picks(a + b, part, &sum);
-        if (above < want && want <= above + a + b) {
-          const bool second = want > above + b;
-          found[0] = x + (second ? 0 : 1);
-          found[1] = want - above - (second ? b : 0);
-        }
-        __syncthreads();
-        lo += found[0] << low;
-        want = found[1];
-        if (low == 0) break;
-        hi = min(hi, lo + ((1u << low) - 1));
-        bits = low;
-        __syncthreads();
+  lo = last_lane(wave_scan(lo, 0xFFFFFFFFu, [](uint32_t x, uint32_t y) { return min(x, y); }));
+  hi = last_lane(wave_scan(hi, 0u, [](uint32_t x, uint32_t y) { return max(x, y); }));
+  if (lane == 0) {
+    ends[wave] = lo;
+    ends[W + wave] = hi;
+  }
+  scan_threads<W>(some, part, sums);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    lo = min(lo, ends[w]);
+    hi = max(hi, ends[W + w]);
+  }
+  const bool every = sums[0] <= budget;
+  uint32_t least = kKeyNan, ties = 0, want = budget - sums[1];   // taken: keys above least, and the first `ties` at it
+  if (!every && want > 0) {
+    // want of the keys lo + [0, 2^bits), in which more than that lie
+    int bits = 32 - __clz((int)max(hi - lo, 1u));
+    for (;;) {
+      const int low = max(bits - kDigit, 0);
+      const uint32_t top = hi - lo;
+      each([&](uint32_t k) {
+        if (k >= lo && k - lo <= top && k != kKeyKeep) atomicAdd(&count[(k - lo) >> low], 1u);
+      });
+      __syncthreads();
+      // from the highest digit down: thread t has digits x + 1 and x
+      const int x = 2 * (kPickThreads - 1 - tid);
+      const uint32_t b = count[x + 1], a = count[x];
+      uint32_t above[1] = {a + b}, sum[1];
+      scan_threads<W>(above, part, sum);
+      count[x + 1] = count[x] = 0;
+      if (above[0] < want && want <= above[0] + a + b) {
+        const bool second = want > above[0] + b;
+        found[0] = x + (second ? 0 : 1);
+        found[1] = want - above[0] - (second ? b : 0);
+        found[2] = second ? a : b;
       }
-      least = lo;
-      ties = want;
+      __syncthreads();
+      lo += found[0] << low;
+      want = found[1];
+      if (low == 0) {
+        least = lo;
+        ties = want;
+        break;
+      }
+      if (want == found[2]) {      // all of this digit's keys
+        least = lo - 1;
+        break;
+      }
+      hi = min(hi, lo + ((1u << low) - 1));
+      bits = low;
     }
   }
   // 16 bits each: taken for sure, and ties, of this thread's keys of one span
   uint32_t done = 0, tied = 0;
   for (int base = 0; base < n; base += span) {
-    if (base || n > span) read(base);
-    uint32_t mine = 0;
-    const bool every = n_valid <= (uint32_t)sel.budget;
+    if (n > span) read(base);
+    uint32_t mine[1] = {0}, sum[1];
 #pragma unroll
-    for (int x = 0; x < kOwn; ++x) mine += every ? (own[x] != 0) : (own[x] > least ? 1u : 0u) + (own[x] == least ? 1u << 16 : 0u);
-    uint32_t sum;
-    const uint32_t before = scan_picks(mine, part, &sum);
-    uint32_t at_tie = tied + (before >> 16), at = done + (before & 0xFFFFu) + min(at_tie, ties);
+    for (int x = 0; x < kOwn; ++x) mine[0] += every ? (own[x] != 0) : (own[x] > least ? 1u : 0u) + (own[x] == least ? 1u << 16 : 0u);
+    scan_threads<W>(mine, part, sum);
+    uint32_t at_tie = tied + (mine[0] >> 16), at = done + (mine[0] & 0xFFFFu) + min(at_tie, ties);
 #pragma unroll
     for (int x = 0; x < kOwn; ++x) {
       const bool tie = !every && own[x] == least;
@@ -477,10 +481,10 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_r
       if (tie) ++at_tie;
       if (take) out[at++] = base + tid * kOwn + x;
     }
-    done += sum & 0xFFFFu;
-    tied += sum >> 16;
+    done += sum[0] & 0xFFFFu;
+    tied += sum[0] >> 16;
   }
-  for (uint32_t j = done + min(tied, ties) + tid; j < (uint32_t)sel.budget; j += kPickThreads) out[j] = -1;
+  for (uint32_t j = done + min(tied, ties) + tid; j < budget; j += kPickThreads) out[j] = -1;
 }
 
 int grid_for(int64_t n, int most) { return (int)std::min<int64_t>(std::max<int64_t>(n, 1), most); }
@@ -492,7 +496,7 @@ int launch_page_tables(const kvtc_page_plan& a, hipStream_t s) {
   const int grid = grid_for((runs + kPageThreads - 1) / kPageThreads, 1024);
   const size_t lds = tables_lds_bytes(a.n_requests);
   allow_lds(tables_kernel, lds + 256);     // with what the kernel declares itself
-  hipLaunchKernelGGL(tables_kernel, dim3(grid), dim3(kPageThreads), lds, s, a);
+  hipLaunchKernelGGL(tables_kernel, dim3(grid), dim3(kPageThreads), lds, s, a, block_div(a.block_size));
   return (int)hipGetLastError();
 }
 
@@ -515,9 +519,9 @@ int launch_page_bounds(const kvtc_pages& p, const kvtc_requests& r, const int32_
   const int grid = grid_for((int64_t)r.n_requests * r.table_width * slabs / (kPageThreads / 64) + 1, 2048);
   const size_t lds = (size_t)r.n_requests * 4;
   if (p.dtype == KVTC_F32)
-    hipLaunchKernelGGL(bounds_kernel<float>, dim3(grid), dim3(kPageThreads), lds, s, p, r, from, (float*)bounds);
+    hipLaunchKernelGGL(bounds_kernel<float>, dim3(grid), dim3(kPageThreads), lds, s, p, r, block_div(p.block_size), from, (float*)bounds);
   else
-    hipLaunchKernelGGL(bounds_kernel<uint16_t>, dim3(grid), dim3(kPageThreads), lds, s, p, r, from, (uint16_t*)bounds);
+    hipLaunchKernelGGL(bounds_kernel<uint16_t>, dim3(grid), dim3(kPageThreads), lds, s, p, r, block_div(p.block_size), from, (uint16_t*)bounds);
   return (int)hipGetLastError();
 }
 
@@ -531,14 +535,16 @@ void launch_scores(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queri
   const int64_t most = (int64_t)r.n_requests * p.kv_heads * r.table_width, step = kPageThreads / lp;
   const int64_t span = std::min<int64_t>(16, std::max<int64_t>(1, most / (4096 * step))) * step;
   const dim3 grid((unsigned)((r.table_width + span - 1) / span), p.kv_heads, r.n_requests);
-  hipLaunchKernelGGL(score_kernel<T>, grid, dim3(kPageThreads), 0, s, p, r, q, (const T*)bounds, sel, keys, (int)span, lp);
+  hipLaunchKernelGGL(score_kernel<T>, grid, dim3(kPageThreads), 0, s, p, r, q, (const T*)bounds,
+                     block_div(p.block_size), sel, keys, (int)span, lp);
 }
 
 int launch_page_select(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q, const void* bounds,
                        const kvtc_selection& sel, void* ws, hipStream_t s) {
   if (p.dtype == KVTC_F32) launch_scores<float>(p, r, q, bounds, sel, (uint32_t*)ws, s);
   else launch_scores<uint16_t>(p, r, q, bounds, sel, (uint32_t*)ws, s);
-  hipLaunchKernelGGL(pick_kernel, dim3(p.kv_heads, r.n_requests), dim3(kPickThreads), 0, s, p, r, sel, (const uint32_t*)ws);
+  hipLaunchKernelGGL(pick_kernel, dim3(p.kv_heads, r.n_requests), dim3(kPickThreads), 0, s, p, r,
+                     block_div(p.block_size), sel, (const uint32_t*)ws);
   return (int)hipGetLastError();
 }
 
