@@ -42,57 +42,108 @@ struct AttendArgs {
 // gt sums of weights.
 __host__ __device__ constexpr size_t part_floats(int gt, int dp) { return (size_t)gt * (dp + 2); }
 
-// One wave's tile: positions [P, P + TK) of a row in the lanes' registers,
-// lane l = 16 g + r.
+// One wave's tile: positions [P, P + TK) of a row, in TK / TG = 4 groups of TG.
+// Lane l = 16 g + r.
 //
 // bf16, TK = 32, v_mfma_f32_16x16x32_bf16 (16 rows x 32 deep, lane l gives
-// row r, depth 8 g .. + 8): first product S^T = K q^T, two blocks of 16 keys;
-// block t's row r is position 8 (r / 4) + 4 t + r % 4, so that the result,
-// rows 4 g + i of query r, is positions 8 g + 4 t + i: exactly the depths 8 g ..
-// + 8 that the lane gives as the second product's operand. out^T = V^T p^T: the lane loads positions 8 g .. + 8, 16 bytes
-// (dims 8 r .. + 8) of each, whole 256-byte rows per instruction, and transposes
-// 8 x 8 in registers; product j yields dims 8 r' + j of query r in rows r'.
+// row r, depth 8 g .. + 8): the first product is S^T = K q^T in two blocks of
+// 16 keys; block t's row r is position 4 t + r % 4 of group r / 4, so that the
+// result, rows 4 g + i of query r, is positions 4 t + i of group g: exactly the
+// depths that the lane gives as the second product's operand. That is
+// out^T = V^T p^T: the lane loads the rows of group g, 16 bytes (dims 8 r ..
+// + 8) of each, whole 256-byte rows per instruction, and transposes 8 x 8 in
+// registers; product j yields dims 8 r' + j of query r in its rows r'.
 //
-// f32, TK = 16, v_mfma_f32_16x16x4_f32 (lane gives row r, depth g): key row
-// r is position r, depths in the order the 16-byte loads bring; the result's
-// rows 4 g + i are the positions whose values the lane loads.
+// f32, TK = 16, v_mfma_f32_16x16x4_f32 (lane l gives row r, depth g): key row r
+// is position r % 4 of group r / 4, the depths in the order that 16-byte reads
+// bring; the result's rows 4 g + i are the positions whose values the lane has.
+//
+// Values are read past the caches (each is used once) straight into registers.
+// The keys' operand wants 64 bytes of each of 16 rows, half a cache line, which
+// such reads fetch twice (8 x 64K tokens: 386 us against 359 with cached key
+// reads), so keys go to LDS first, whole rows an instruction and without a
+// register, and come back as operands: CPR pieces of 16 bytes a row, exchanged
+// within each row (place) so that eight lanes' reads meet all banks.
+template <class T, int DP>
+struct Keys {
+  static constexpr int KR = sizeof(T) == 2 ? 2 : 1, TG = 4 * KR, EL = 16 / sizeof(T), CPR = DP / EL;
+  static constexpr int kNt = 2;                    // the non-temporal bit of a load
+  static constexpr int RPI = 64 / CPR, NX = 16 * KR / RPI, BYTES = 16 * KR * CPR * 16;
+  // The tile's position (in order) that lane l fetches with instruction x.
+  __device__ __forceinline__ static constexpr int at(int x, int l) { return x * RPI + l / CPR; }
+  __device__ __forceinline__ static int place(int pos, int c) {
+    return c ^ (KR == 2 ? (pos & 3) | ((pos >> 3) & 1) << 2 : pos & 7);
+  }
+  __device__ __forceinline__ static int elem(int x, int l, int D) {      // of the row, that lane l fetches
+    const int d = place(at(x, l), l % CPR) * EL;
+    return d < D ? d : 0;
+  }
+  // Rows of whole groups: an instruction's rows lie in one group, whose first
+  // row is group(y), the same for all lanes; `row` bytes apart.
+  template <class Group>
+  __device__ __forceinline__ static void load_groups(uint8_t* buf, Group group, int row, int D, int l) {
+    static_assert(RPI <= TG, "one group an instruction");
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc((void*)group(x * RPI / TG), 0, TG * row, 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rows, (__attribute__((address_space(3))) void*)(buf + 1024 * x), 16,
+                                               (l / CPR) * row + elem(x, l, D) * (int)sizeof(T), (x * RPI % TG) * row, 0, kNt);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // Rows anywhere: row(x) is the lane's for instruction x.
+  template <class Row>
+  __device__ __forceinline__ static void load_rows(uint8_t* buf, Row row, int D, int l) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < NX; ++x)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(row(x) + elem(x, l, D)),
+                                       (__attribute__((address_space(3))) void*)(buf + 1024 * x), 16, 0, kNt);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // The copies to LDS are counted like loads, but the compiler does not wait
+  // for them before it reads LDS, nor for its reads before a copy overwrites
+  // them: landed<N>() after N loads that follow the copies, and free().
+  template <int N>
+  __device__ __forceinline__ static void landed() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ __forceinline__ static void free() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // operand piece s (dims 4 EL s + EL g .. + EL) of block t's row r; dims past
+  // D meet zeros of q, but a NaN must not
+  __device__ __forceinline__ static u32x4 piece(const uint8_t* buf, int t, int s, int D, int g, int r) {
+    const int pos = TG * (r >> 2) + 4 * t + (r & 3);
+    const u32x4 k = *(const u32x4*)(buf + (pos * CPR + place(pos, 4 * s + g)) * 16);
+    return D == DP || (4 * s + g) * EL < D ? k : u32x4{0, 0, 0, 0};
+  }
+};
+
 template <class T, int DP> struct Tile;
 
 template <int DP>
 struct Tile<uint16_t, DP> {
+  typedef Keys<uint16_t, DP> KK;
   static constexpr int TK = 32, TG = 8, KS = DP / 32, VB = DP >= 128 ? DP / 128 : 1, VW = DP >= 128 ? 4 : 2, ND = 2 * VW;
   static constexpr int OUT = VB * ND;                 // accumulators of 4 (out^T)
   typedef uint32_t vvec __attribute__((ext_vector_type(VW)));
-  u32x4 k[2][KS];
   vvec v[TG][VB];
-  // the head's elements of the lane's key rows and value rows
-  static constexpr int KR = 2;
-  __device__ __forceinline__ static int key_at(int t, int r) { return 4 * t + (r & 3); }   // of its group
-  template <class KP>
-  __device__ __forceinline__ void load_keys(KP kp, int D, int g) {
-#pragma unroll
-    for (int t = 0; t < KR; ++t)
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int d = 32 * s + 8 * g;
-        k[t][s] = *(const u32x4*)(kp(t) + (d < D ? d : 0));
-      }
-  }
-  template <class VP>
-  __device__ __forceinline__ void load_values(VP vp, int D, int r) {
+  // row(e): the head's elements of position e of the lane's group; dims past D are never stored
+  template <class Row>
+  __device__ __forceinline__ void load_values(Row row, int D, int r) {
 #pragma unroll
     for (int e = 0; e < TG; ++e)
 #pragma unroll
       for (int b = 0; b < VB; ++b) {
         const int d = 128 * b + ND * r;
-        v[e][b] = *(const vvec*)(vp(e) + (d < D ? d : 0));
+        v[e][b] = __builtin_nontemporal_load((const vvec*)(row(e) + (d < D ? d : 0)));
       }
-  }
-  // dims past D: zero in K (they meet zeros of q, but a NaN must not), never stored from V
-  __device__ __forceinline__ void mask_dims(int D, int g) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-      if (32 * s + 8 * g >= D) k[0][s] = k[1][s] = u32x4{0, 0, 0, 0};
   }
   // positions whose bit of live is clear are not attended to: their weight is 0, but 0 x NaN is not
   __device__ __forceinline__ void mask_rows(uint32_t live) {
@@ -112,15 +163,24 @@ struct Tile<uint16_t, DP> {
       }
     }
   };
-  __device__ __forceinline__ void scores(const Query& q, float* s) const {
+  __device__ __forceinline__ static void scores(const Query& q, const uint8_t* keys, float* s, int D, int g, int r) {
+    u32x4 k[2][KS];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      f32x4 a = {0, 0, 0, 0};
+    for (int i = 0; i < KS; ++i) {
+      k[0][i] = KK::piece(keys, 0, i, D, g, r);
+      k[1][i] = KK::piece(keys, 1, i, D, g, r);
+    }
+    KK::free();
+    f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
-        a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[t][i]), __builtin_bit_cast(bf16x8, q.f[i]), a, 0, 0, 0);
+    for (int i = 0; i < KS; ++i) {
+      a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[0][i]), __builtin_bit_cast(bf16x8, q.f[i]), a, 0, 0, 0);
+      b = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[1][i]), __builtin_bit_cast(bf16x8, q.f[i]), b, 0, 0, 0);
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[4 * t + i] = a[i];
+    for (int i = 0; i < 4; ++i) {
+      s[i] = a[i];
+      s[4 + i] = b[i];
     }
   }
   // The weights enter as two bf16 terms: 16 bits of them, where a single
@@ -157,34 +217,19 @@ struct Tile<uint16_t, DP> {
 
 template <int DP>
 struct Tile<float, DP> {
+  typedef Keys<float, DP> KK;
   static constexpr int TK = 16, TG = 4, KS = DP / 16, VB = DP / 64, ND = 4;
   static constexpr int OUT = VB * ND;
-  f32x4 k[KS];
   f32x4 v[TG][VB];
-  static constexpr int KR = 1;
-  __device__ __forceinline__ static int key_at(int, int r) { return r & 3; }
-  template <class KP>
-  __device__ __forceinline__ void load_keys(KP kp, int D, int g) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d = 16 * s + 4 * g;
-      k[s] = *(const f32x4*)(kp(0) + (d < D ? d : 0));
-    }
-  }
-  template <class VP>
-  __device__ __forceinline__ void load_values(VP vp, int D, int r) {
+  template <class Row>
+  __device__ __forceinline__ void load_values(Row row, int D, int r) {
 #pragma unroll
     for (int e = 0; e < TG; ++e)
 #pragma unroll
       for (int b = 0; b < VB; ++b) {
         const int d = 64 * b + ND * r;
-        v[e][b] = *(const f32x4*)(vp(e) + (d < D ? d : 0));
+        v[e][b] = __builtin_nontemporal_load((const f32x4*)(row(e) + (d < D ? d : 0)));
       }
-  }
-  __device__ __forceinline__ void mask_dims(int D, int g) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-      if (16 * s + 4 * g >= D) k[s] = f32x4{0, 0, 0, 0};
   }
   __device__ __forceinline__ void mask_rows(uint32_t live) {
 #pragma unroll
@@ -203,7 +248,11 @@ struct Tile<float, DP> {
       }
     }
   };
-  __device__ __forceinline__ void scores(const Query& q, float* s) const {
+  __device__ __forceinline__ static void scores(const Query& q, const uint8_t* keys, float* s, int D, int g, int r) {
+    f32x4 k[KS];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) k[i] = __builtin_bit_cast(f32x4, KK::piece(keys, 0, i, D, g, r));
+    KK::free();
     f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};      // two chains: one would wait for each result
 #pragma unroll
     for (int i = 0; i < KS; ++i)
@@ -236,38 +285,34 @@ __device__ __forceinline__ float sum_groups(float x) {
   return x + __shfl_xor(x, 32, 64);
 }
 
-// One lane's lookups of a tile: the rows of its key group and value group, or
-// with pages that cut groups of each row of them, and which positions of the
-// value group (the score group too) are attended to.
-template <class TT, bool GROUPED>
-struct Places {
-  int32_t k[GROUPED ? 1 : TT::KR], v[GROUPED ? 1 : TT::TG];
-  uint32_t live;
-};
-
 // DP: head_dim rounded up to 64, 128 or 256. GROUPED: every page holds whole
-// groups of TG positions (block_size is a multiple), so a lane looks up two
-// pages a tile and not one for each of its rows.
+// groups of TG positions (block_size is a multiple), so a lane looks up one
+// page a tile, its group's, and not one for each of its rows.
 //
-// The next tile's keys are loaded into the registers of this one's as soon as
-// the scores are computed, its values after the second product; the pages of
-// the one after are looked up before them, so that no wait for a lookup waits
-// for data behind it. One set of registers leaves room for more waves.
+// The next tile's keys are loaded as soon as this one's scores are computed,
+// its values after the second product, so one set of registers and one buffer
+// a wave keep loads in flight and leave room for more waves. Lookups run ahead
+// by a tile for each load in their chain, and are only looked at when they
+// are needed: a wait for one would be a wait for all data loaded before it.
+// (Without whole groups there are too many to hold; they are waited for.)
 template <class T, int DP, bool GROUPED>
 __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(AttendArgs a) {
   typedef Tile<T, DP> TT;
-  typedef Places<TT, GROUPED> PL;
+  typedef Keys<T, DP> KK;
   constexpr int TK = TT::TK, TG = TT::TG, CH = NW * TK, NS = TK / 4;
+  constexpr int NL = GROUPED ? 1 : TG + KK::NX;       // lookups of a lane: its group, or its value rows and its key rows
   constexpr uint32_t kFull = (1u << TG) - 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ uint32_t scan_part[NW];
   __shared__ float wm[NW][16], wl[NW][16];
-  float* wo = (float*)lds;                                              // [NW][gt][DP]
-  uint32_t* pre = (uint32_t*)(lds + (size_t)NW * a.gt * DP * 4);        // chunks of the requests before each one, per row
+  static_assert(KK::BYTES == 16 * DP * 4, "a wave's sums take the place of its keys");
+  float* wo = (float*)lds;                                              // [NW][16][DP]
+  uint32_t* pre = (uint32_t*)(lds + NW * KK::BYTES);                    // chunks of the requests before each one, per row
   int32_t* lens = (int32_t*)pre + a.r.n_requests;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
   const int n_req = a.r.n_requests, bs = a.p.block_size, D = a.p.head_dim, rows_each = a.p.kv_heads * a.tiles;
   const int64_t F = (int64_t)a.p.kv_heads * D;
+  uint8_t* keys = lds + wave * KK::BYTES;
 
   // positions of a request: its tokens, or those of as many selected pages as it has pages
   auto positions = [&](int len) -> int { return a.sel.blocks ? min(a.sel.budget, pages_of(len, a.div)) * bs : len; };
@@ -318,53 +363,58 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
     const T* kh = (const T*)a.p.k + h * D;
     const T* vh = (const T*)a.p.v + h * D;
 
-    // the row of a position (the first of its group) and how many tokens lie from there on, 0 for none
-    auto place = [&](int pos, int32_t* row_at) -> int {
-      *row_at = 0;
-      if (pos >= n_pos) return 0;
-      const uint32_t slot = div_block(pos, a.div);
-      const int off = pos - (int)slot * bs;
-      const int j = list ? list[slot] : (int)slot;
-      if (j < 0 || j >= n_pages) return 0;
-      const int id = table[j];
+    // A position's page, in steps between which a load is on its way: the entry
+    // of the table (from the list, or the page's index), the entry's page, and
+    // from that the position's row and the number of tokens from there on.
+    auto pos_of = [&](uint32_t ch, int x) -> int {
+      const int P = (int)ch * CH + wave * TK;
+      return x < TG ? P + TG * g + x : P + KK::at(x - TG, lane);
+    };
+    auto entry_of = [&](uint32_t ch, int x) -> int {
+      const int slot = (int)div_block(min(pos_of(ch, x), n_pos - 1), a.div);
+      return list ? list[slot] : slot;
+    };
+    auto page_of = [&](int entry) -> int { return table[entry >= 0 && entry < n_pages ? entry : 0]; };
+    bool bad = false;
+    auto row_of = [&](uint32_t ch, int x, int entry, int id, int* left) -> int {
+      const int pos = pos_of(ch, x), off = pos - (int)div_block(min(pos, n_pos - 1), a.div) * bs;
+      *left = 0;
+      if (pos >= n_pos || entry < 0 || entry >= n_pages) return 0;
       if (id < 0 || id >= a.p.n_blocks) {
-        set_status(a.r.status, i, KVTC_E_INVALID);
+        bad = true;
         return 0;
       }
-      *row_at = id * bs + off;
-      return max(len - (j * bs + off), 0);
-    };
-    auto look_up = [&](uint32_t ch) -> PL {
-      const int P = (int)ch * CH + wave * TK, kg = P + TG * (r >> 2), vg = P + TG * g;
-      PL w;
-      if constexpr (GROUPED) {
-        (void)place(kg, &w.k[0]);
-        const int left = place(vg, &w.v[0]);
-        w.live = left >= TG ? kFull : (1u << left) - 1;
-      } else {
-        w.live = 0;
-#pragma unroll
-        for (int x = 0; x < TT::KR; ++x) (void)place(kg + TT::key_at(x, r), &w.k[x]);
-#pragma unroll
-        for (int e = 0; e < TG; ++e) w.live |= place(vg + e, &w.v[e]) > 0 ? 1u << e : 0u;
-      }
-      return w;
+      *left = max(len - (entry * bs + off), 0);
+      return id * bs + off;
     };
     TT t;
-    auto load_keys = [&](const PL& w) {
-      if constexpr (GROUPED) {
-        const T* kp = kh + w.k[0] * F;
-        t.load_keys([&](int x) { return kp + TT::key_at(x, r) * F; }, D, g);
-      } else {
-        t.load_keys([&](int x) { return kh + w.k[x] * F; }, D, g);
+    int row_at[NL];
+    uint32_t live = 0;
+    // rows of a tile's positions, and which positions of the lane's group are attended to
+    auto resolve = [&](uint32_t ch, const int* entry, const int* id) -> uint32_t {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int x = 0; x < NL; ++x) {
+        int left;
+        row_at[x] = row_of(ch, x, entry[x], id[x], &left);
+        if (GROUPED) bits = left >= TG ? kFull : (1u << left) - 1;
+        else if (x < TG) bits |= left > 0 ? 1u << x : 0u;
       }
+      return bits;
     };
-    auto load_values = [&](const PL& w) {
+    auto load_keys = [&]() {
+      if constexpr (GROUPED)
+        KK::load_groups(keys, [&](int y) { return kh + (int64_t)__builtin_amdgcn_readlane(row_at[0], 16 * y) * F; },
+                        (int)(F * sizeof(T)), D, lane);
+      else
+        KK::load_rows(keys, [&](int x) { return kh + (int64_t)row_at[TG + x] * F; }, D, lane);
+    };
+    auto load_values = [&]() {
       if constexpr (GROUPED) {
-        const T* vp = vh + w.v[0] * F;
-        t.load_values([&](int e) { return vp + e * F; }, D, r);
+        const T* first = vh + (int64_t)row_at[0] * F;
+        t.load_values([&](int e) { return first + e * F; }, D, r);
       } else {
-        t.load_values([&](int e) { return vh + w.v[e] * F; }, D, r);
+        t.load_values([&](int e) { return vh + (int64_t)row_at[e] * F; }, D, r);
       }
     };
     typename TT::Query q;
@@ -372,20 +422,30 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
     float m = -INFINITY, l = 0.0f;
     f32x4 o[TT::OUT];
 
-    PL now = look_up(c0);
-    q.load((const T*)a.q.q + i * a.q.q_stride + q_at + (int64_t)r * D, D, g, r < nq);
+    // of the next tile, and of the one after (GROUPED)
+    int entry[NL], id[NL], entry2 = 0;
+    auto look_up = [&](uint32_t ch) {
 #pragma unroll
-    for (int j = 0; j < TT::OUT; ++j) o[j] = f32x4{0, 0, 0, 0};
-    PL next = look_up(c0 + 1);
-    load_keys(now);
-    load_values(now);
-    for (uint32_t ch = c0; ch < c1; ++ch) {
-      const uint32_t live = now.live;
-      const PL after = look_up(ch + 2);
-      if (D != DP) t.mask_dims(D, g);
+      for (int x = 0; x < NL; ++x) entry[x] = entry_of(ch, x);
+#pragma unroll
+      for (int x = 0; x < NL; ++x) id[x] = page_of(entry[x]);
+    };
+    // Chunk ch, whose loads are on their way; `more` loads the next one's.
+    auto tile = [&](uint32_t ch, auto more) {
+      uint32_t live_next = 0;
+      if constexpr (more) {
+        if constexpr (!GROUPED) look_up(ch + 1);
+        live_next = resolve(ch + 1, entry, id);
+        if constexpr (GROUPED) {
+          entry[0] = entry2;
+          id[0] = page_of(entry2);
+          entry2 = entry_of(ch + 3, 0);
+        }
+      }
       float s[NS];
-      t.scores(q, s);
-      if (ch + 1 < c1) load_keys(next);
+      KK::template landed<TG * TT::VB + (more && GROUPED ? 1 : 0)>();
+      TT::scores(q, keys, s, D, g, r);
+      if constexpr (more) load_keys();
 #pragma unroll
       for (int e = 0; e < NS; ++e) s[e] *= c;
       if (__any(live != kFull)) {
@@ -414,10 +474,24 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
         l += s[e];
       }
       t.add_values(s, o);
-      if (ch + 1 < c1) load_values(next);
-      now = next;
-      next = after;
+      if constexpr (more) load_values();
+      live = live_next;
+    };
+    look_up(c0);
+    q.load((const T*)a.q.q + i * a.q.q_stride + q_at + (int64_t)r * D, D, g, r < nq);
+#pragma unroll
+    for (int j = 0; j < TT::OUT; ++j) o[j] = f32x4{0, 0, 0, 0};
+    live = resolve(c0, entry, id);
+    if constexpr (GROUPED) {
+      entry[0] = entry_of(c0 + 1, 0);
+      entry2 = entry_of(c0 + 2, 0);
+      id[0] = page_of(entry[0]);
     }
+    load_keys();
+    load_values();
+    for (uint32_t ch = c0; ch + 1 < c1; ++ch) tile(ch, std::true_type{});
+    tile(c1 - 1, std::false_type{});
+    if (bad) set_status(a.r.status, i, KVTC_E_INVALID);
 
     // join the waves
     l = sum_groups(l);
@@ -437,7 +511,7 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int j = 0; j < TT::ND; ++j)
-            wo[((size_t)wave * a.gt + r) * DP + b * 16 * TT::ND + (4 * g + x) * TT::ND + j] = o[b * TT::ND + j][x] * f;
+            wo[((size_t)wave * 16 + r) * DP + b * 16 * TT::ND + (4 * g + x) * TT::ND + j] = o[b * TT::ND + j][x] * f;
     }
     __syncthreads();
     const bool whole = c0 == 0 && c1 == n;
@@ -451,7 +525,7 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
       const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        v += *(const f32x4*)(wo + ((size_t)w * a.gt + qr) * DP + d);
+        v += *(const f32x4*)(wo + ((size_t)w * 16 + qr) * DP + d);
         sum += wl[w][qr] * __builtin_amdgcn_exp2f(wm[w][qr] - base);
       }
       if (whole) {
@@ -536,7 +610,7 @@ __global__ void __launch_bounds__(kPageThreads) join_kernel(AttendArgs a) {
 
 template <class T, int DP, bool GROUPED>
 void launch_pieces(const AttendArgs& a, uint32_t grid, hipStream_t s) {
-  const size_t lds = (size_t)NW * a.gt * DP * 4 + (size_t)a.r.n_requests * 8;
+  const size_t lds = (size_t)NW * Keys<T, DP>::BYTES + (size_t)a.r.n_requests * 8;
   allow_lds(attend_kernel<T, DP, GROUPED>, lds + 1024);      // with what the kernel declares itself
   hipLaunchKernelGGL((attend_kernel<T, DP, GROUPED>), dim3(grid), dim3(kPageThreads), lds, s, a);
 }
