@@ -22,7 +22,6 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int NW = kPageThreads / 64;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct AttendArgs {
@@ -295,8 +294,12 @@ __device__ __forceinline__ float sum_groups(float x) {
 // by a tile for each load in their chain, and are only looked at when they
 // are needed: a wait for one would be a wait for all data loaded before it.
 // (Without whole groups there are too many to hold; they are waited for.)
+template <class T, int DP>
+constexpr int kWavesOf = attend_waves(sizeof(T) == 4 ? KVTC_F32 : KVTC_BF16, DP);
+
 template <class T, int DP, bool GROUPED>
-__global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(AttendArgs a) {
+__global__ void __launch_bounds__((64 * kWavesOf<T, DP>), (kWavesOf<T, DP> / 4)) attend_kernel(AttendArgs a) {
+  constexpr int NW = kWavesOf<T, DP>, kThreads = 64 * NW;
   typedef Tile<T, DP> TT;
   typedef Keys<T, DP> KK;
   constexpr int TK = TT::TK, TG = TT::TG, CH = NW * TK, NS = TK / 4;
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
   __shared__ float wm[NW][16], wl[NW][16];
   static_assert(KK::BYTES == 16 * DP * 4, "a wave's sums take the place of its keys");
   float* wo = (float*)lds;                                              // [NW][16][DP]
-  uint32_t* pre = (uint32_t*)(lds + NW * KK::BYTES);                    // chunks of the requests before each one, per row
+  uint32_t* pre = (uint32_t*)(lds + NW * KK::BYTES);                    // units of the requests before each one, per row
   int32_t* lens = (int32_t*)pre + a.r.n_requests;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
   const int n_req = a.r.n_requests, bs = a.p.block_size, D = a.p.head_dim, rows_each = a.p.kv_heads * a.tiles;
@@ -316,9 +319,12 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
 
   // positions of a request: its tokens, or those of as many selected pages as it has pages
   auto positions = [&](int len) -> int { return a.sel.blocks ? min(a.sel.budget, pages_of(len, a.div)) * bs : len; };
-  uint32_t total;
+  // A row counts as its chunks, and one that a range holds with others as
+  // kAttendRow more: so much longer its start and end take.
+  uint32_t total, range;
+  auto extra = [&](uint32_t n) -> uint32_t { return n < range ? kAttendRow : 0u; };
   {
-    const int each = (n_req + kPageThreads - 1) / kPageThreads, i0 = threadIdx.x * each, i1 = min(i0 + each, n_req);
+    const int each = (n_req + kThreads - 1) / kThreads, i0 = threadIdx.x * each, i1 = min(i0 + each, n_req);
     uint32_t scan[1] = {0}, sum[1];
     for (int i = i0; i < i1; ++i) {
       int len = checked_len(a.r, bs, i);
@@ -331,16 +337,23 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
       scan[0] += pre[i];
     }
     scan_threads<NW>(scan, scan_part, sum);
+    range = sum[0] * rows_each / gridDim.x;
+    scan[0] = 0;
+    for (int i = i0; i < i1; ++i) scan[0] += pre[i] ? pre[i] + extra(pre[i]) : 0u;
+    scan_threads<NW>(scan, scan_part, sum);
     for (int i = i0; i < i1; ++i) {
       const uint32_t n = pre[i];
       pre[i] = scan[0];
-      scan[0] += n;
+      scan[0] += n ? n + extra(n) : 0u;
     }
     total = sum[0] * rows_each;
   }
   __syncthreads();
-  const uint32_t per = (total + gridDim.x - 1) / gridDim.x;
-  const uint32_t u0 = min(blockIdx.x * per, total), u1 = min(u0 + per, total);
+  // Range w of as many as there are units for starts at floor(w total / ranges):
+  // equal rows then end where ranges do whenever they can, and no range is empty.
+  const uint32_t ranges = max(min(gridDim.x, total), 1u), share = total / ranges, rest = total - share * ranges;
+  auto start_of = [&](uint32_t w) -> uint32_t { return w * share + w * rest / ranges; };
+  const uint32_t u0 = start_of(min(blockIdx.x, ranges)), u1 = start_of(min(blockIdx.x + 1, ranges));
   // requests without a token have no chunk
   for (int i = blockIdx.x * NW + wave; i < n_req; i += gridDim.x * NW)
     if (lens[i] == 0) {
@@ -350,12 +363,18 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
   uint4 meta = {0, 0, 0, 0};
 
   for (uint32_t u = u0; u < u1;) {
-    // the row: request i, KV head h, query tile qt; its chunks [c0, c1) of n
+    // the row: request i, KV head h, query tile qt; of its units, `more` and
+    // its n chunks, [off, end), of its chunks [c0, c1)
     const int i = owner_of(pre, n_req, u / rows_each);
     const int len = lens[i], n_pos = positions(len), n_pages = pages_of(len, a.div);
-    const uint32_t n = (uint32_t)((n_pos + CH - 1) / CH), at = u - pre[i] * rows_each, row = at / n;
+    const uint32_t n = (uint32_t)((n_pos + CH - 1) / CH), at = u - pre[i] * rows_each;
+    const uint32_t more = extra(n), row = at / (n + more), off = at - row * (n + more), end = min(n + more, off + (u1 - u));
+    const uint32_t c0 = off > more ? off - more : 0u, c1 = end > more ? end - more : 0u;
+    if (c0 == c1) {
+      u += end - off;
+      continue;
+    }
     const int h = (int)row / a.tiles, qt = (int)row % a.tiles;
-    const uint32_t c0 = at - row * n, c1 = min(n, c0 + (u1 - u));
     const int nq = min(16, a.group - 16 * qt);
     const int32_t* list = a.sel.blocks ? a.sel.blocks + ((int64_t)i * a.p.kv_heads + h) * a.sel.budget : nullptr;
     const int32_t* table = a.r.block_table + (int64_t)i * a.r.table_stride;
@@ -516,7 +535,7 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
     __syncthreads();
     const bool whole = c0 == 0 && c1 == n;
     float* part = a.part + (2 * (size_t)blockIdx.x + (c0 ? 0 : 1)) * part_floats(a.gt, DP);
-    for (int x = threadIdx.x; x < nq * (DP / 4); x += kPageThreads) {
+    for (int x = threadIdx.x; x < nq * (DP / 4); x += kThreads) {
       const int qr = x / (DP / 4), d = x % (DP / 4) * 4;
       f32x4 v = {0, 0, 0, 0};
       float top = -INFINITY, sum = 0.0f;
@@ -545,12 +564,20 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
         }
       }
     }
-    // The range starts inside this row, and the row began in the range before: this workgroup's entry tells
-    // join_kernel the row and the last range it reaches.
-    if (u == u0 && c0 > 0 && c0 <= per)
-      meta = uint4{1u + (uint32_t)i, row, (u - c0 + n - 1) / per, 0};
+    // The range starts inside this row's chunks, and their first one lies in the range before: this workgroup's
+    // entry tells join_kernel the row and the last range it reaches.
+    if (u == u0 && c0 > 0 && c0 <= u0 - start_of(blockIdx.x - 1)) {
+      const uint32_t tail = u0 - c0 + n - 1;     // the row's last unit
+      uint32_t lo = blockIdx.x, hi = ranges - 1;
+      while (lo < hi) {
+        const uint32_t mid = (lo + hi + 1) >> 1;
+        if (start_of(mid) <= tail) lo = mid;
+        else hi = mid - 1;
+      }
+      meta = uint4{1u + (uint32_t)i, row, lo, 0};
+    }
     __syncthreads();
-    u += c1 - c0;
+    u += end - off;
   }
   if (threadIdx.x == 0) a.meta[blockIdx.x] = meta;
 }
@@ -560,43 +587,61 @@ __global__ void __launch_bounds__(kPageThreads, DP > 128 ? 1 : 2) attend_kernel(
 // w - 1 and slot 0 of ranges w .. last.
 template <class T, int DP>
 __global__ void __launch_bounds__(kPageThreads) join_kernel(AttendArgs a) {
-  constexpr int LANES = DP / 4, PER = kPageThreads / LANES;     // threads on one piece, pieces at a time
+  constexpr int LANES = DP / 4, PER = kPageThreads / LANES, kAhead = 4;     // threads on one piece, pieces at a time
   __shared__ f32x4 sums[PER][LANES];
-  __shared__ float tops[NW], weights[PER];
+  __shared__ float tops[PER], weights[PER];
   const uint4 meta = a.meta[blockIdx.x];
   const int i = (int)meta.x - 1, h = (int)meta.y / a.tiles, qt = (int)meta.y % a.tiles, qr = blockIdx.y;
   if (i < 0 || qr >= min(16, a.group - 16 * qt)) return;
   const int w0 = (int)blockIdx.x - 1, n = (int)meta.z - w0 + 1, D = a.p.head_dim;
-  auto piece = [&](int x) { return a.part + (2 * (size_t)(w0 + x) + (x ? 0 : 1)) * part_floats(a.gt, DP); };
-  float top = -INFINITY;
-  for (int x = threadIdx.x; x < n; x += kPageThreads) top = fmaxf(top, piece(x)[(size_t)a.gt * DP + qr]);
-#pragma unroll
-  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-  __syncthreads();
-  top = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) top = fmaxf(top, tops[w]);
-  const float base = top == -INFINITY ? 0.0f : top;
   const int d = threadIdx.x % LANES, y = threadIdx.x / LANES;
+  // each thread: pieces y, y + PER, ..., kAhead of them loaded at a time, relative to a maximum of its own
+  float top = -INFINITY, sum = 0.0f;
   f32x4 v = {0, 0, 0, 0};
-  float sum = 0.0f;
-  for (int x = y; x < n; x += PER) {
-    const float* p = piece(x);
-    const float f = __builtin_amdgcn_exp2f(p[(size_t)a.gt * DP + qr] - base);
-    sum += f * p[(size_t)a.gt * (DP + 1) + qr];
-    v += f * *(const f32x4*)(p + (size_t)qr * DP + 4 * d);
+  for (int x0 = y; x0 < n; x0 += kAhead * PER) {
+    f32x4 pv[kAhead];
+    float pm[kAhead], pl[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int x = x0 + k * PER, at = min(x, n - 1);
+      const float* p = a.part + (2 * (size_t)(w0 + at) + (at ? 0 : 1)) * part_floats(a.gt, DP);
+      pv[k] = *(const f32x4*)(p + (size_t)qr * DP + 4 * d);
+      pm[k] = p[(size_t)a.gt * DP + qr];
+      pl[k] = p[(size_t)a.gt * (DP + 1) + qr];
+    }
+    float to = top;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) to = fmaxf(to, pm[k]);
+    const float base = to == -INFINITY ? 0.0f : to, f0 = __builtin_amdgcn_exp2f(top - base);
+    top = to;
+    sum *= f0;
+    v *= f0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (x0 + k * PER >= n) continue;
+      const float f = __builtin_amdgcn_exp2f(pm[k] - base);
+      sum += f * pl[k];
+      v += f * pv[k];
+    }
   }
   sums[y][d] = v;
-  if (d == 0) weights[y] = sum;
+  if (d == 0) {
+    tops[y] = top;
+    weights[y] = sum;
+  }
   __syncthreads();
   if (y) return;
+  top = tops[0];
+#pragma unroll
+  for (int x = 1; x < PER; ++x) top = fmaxf(top, tops[x]);
+  const float base = top == -INFINITY ? 0.0f : top;
   sum = 0.0f;
   v = f32x4{0, 0, 0, 0};
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
-    v += sums[x][d];
-    sum += weights[x];
+    const float f = __builtin_amdgcn_exp2f(tops[x] - base);
+    v += f * sums[x][d];
+    sum += f * weights[x];
   }
   const float z = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int64_t hq = (int64_t)h * a.group + 16 * qt + qr;
@@ -610,9 +655,9 @@ __global__ void __launch_bounds__(kPageThreads) join_kernel(AttendArgs a) {
 
 template <class T, int DP, bool GROUPED>
 void launch_pieces(const AttendArgs& a, uint32_t grid, hipStream_t s) {
-  const size_t lds = (size_t)NW * Keys<T, DP>::BYTES + (size_t)a.r.n_requests * 8;
+  const size_t lds = (size_t)kWavesOf<T, DP> * Keys<T, DP>::BYTES + (size_t)a.r.n_requests * 8;
   allow_lds(attend_kernel<T, DP, GROUPED>, lds + 1024);      // with what the kernel declares itself
-  hipLaunchKernelGGL((attend_kernel<T, DP, GROUPED>), dim3(grid), dim3(kPageThreads), lds, s, a);
+  hipLaunchKernelGGL((attend_kernel<T, DP, GROUPED>), dim3(grid), dim3(64 * kWavesOf<T, DP>), lds, s, a);
 }
 
 template <class T, int DP>

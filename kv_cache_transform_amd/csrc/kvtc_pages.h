@@ -15,16 +15,18 @@ __host__ __device__ inline size_t select_ws_bytes(const kvtc_pages& p, const kvt
   return align_up((size_t)r.n_requests * p.kv_heads * r.table_width * 4, kAlign);
 }
 
-// kvtc_page_attend: positions per chunk of work (four waves' tiles), head_dim
-// as the kernels round it up, and the number of workgroups: two for each of
-// the 256 CUs, or as many as there can be chunks. Sizes alone decide, so that
-// a workspace can be sized without a device.
-constexpr int kAttendWorkers = 512;
-__host__ __device__ inline int attend_chunk(int dtype) { return dtype == KVTC_F32 ? 64 : 128; }
-__host__ __device__ inline int attend_dp(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+// kvtc_page_attend: head_dim as the kernels round it up, waves per workgroup,
+// positions per chunk of work (a tile of 32, in fp32 16, per wave) and the
+// number of workgroups. Sizes alone decide, so that a workspace can be sized
+// without a device.
+constexpr int kAttendWorkers = 256;
+constexpr uint32_t kAttendRow = 2;
+__host__ __device__ constexpr int attend_dp(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+__host__ __device__ constexpr int attend_waves(int dtype, int dp) { return 4; }
+__host__ __device__ constexpr int attend_chunk(int dtype, int dp) { return attend_waves(dtype, dp) * (dtype == KVTC_F32 ? 16 : 32); }
 inline int64_t attend_most_chunks(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q) {
-  const int64_t ch = attend_chunk(p.dtype), rows = (int64_t)p.kv_heads * ((q.q_heads / p.kv_heads + 15) / 16);
-  return r.n_requests * rows * (((int64_t)r.table_width * p.block_size + ch - 1) / ch);
+  const int64_t ch = attend_chunk(p.dtype, attend_dp(p.head_dim)), rows = (int64_t)p.kv_heads * ((q.q_heads / p.kv_heads + 15) / 16);
+  return r.n_requests * rows * (((int64_t)r.table_width * p.block_size + ch - 1) / ch + kAttendRow);
 }
 inline uint32_t attend_workers(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q) {
   const int64_t n = attend_most_chunks(p, r, q);
