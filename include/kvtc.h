@@ -460,9 +460,9 @@ kvtc_status kvtc_lossless_sizes(const void* d_ws, int32_t n_jobs, uint64_t* size
  * there, one without leaves its word as it was.
  *
  * Pages of KVTC_BF16 or KVTC_F32; any block_size; head_dim a multiple of 8
- * up to KVTC_MAX_HEAD_DIM; fewer than 2^31 rows in the pages, tokens in a
- * table row and entries in all table rows; at most KVTC_MAX_JOBS requests per
- * call. Requests may share pages. Page, bounds, q and out pointers are
+ * up to KVTC_MAX_HEAD_DIM; fewer than 2^31 rows in the pages, 2^30 tokens in
+ * a table row and 2^30 entries in all table rows; at most KVTC_MAX_JOBS
+ * requests per call. Requests may share pages. Page, bounds, q and out pointers are
  * 16-byte aligned, strides count elements and are multiples of 8.
  * ---------------------------------------------------------------------- */
 
@@ -488,7 +488,7 @@ typedef struct {
  * block_table[i * table_stride + t / block_size] * block_size + t % block_size.
  * A request with lens[i] < 0 or > table_width * block_size counts as empty
  * and gets status KVTC_E_INVALID. Table entries behind a request's last page
- * are not read. An entry outside [0, n_blocks) leaves its tokens out and gives
+ * are not used. An entry outside [0, n_blocks) leaves its tokens out and gives
  * status KVTC_E_INVALID. */
 typedef struct {
   const int32_t* block_table;  /* device [n_requests, table_stride]          */
@@ -540,7 +540,7 @@ typedef struct {
  * and the status KVTC_E_INVALID. *taken is the number of pages given out, so
  * the caller's next free_from is *free_from + *taken. An *free_from < 0 is
  * read as 0. The outputs may not overlap the inputs. Errors: KVTC_E_INVALID,
- * and KVTC_E_UNSUPPORTED for a cache of 2^31 rows or more. */
+ * KVTC_E_CAPACITY (too many requests) and KVTC_E_UNSUPPORTED (sizes). */
 kvtc_status kvtc_page_tables(const kvtc_page_plan* plan, hipStream_t stream);
 
 /* New rows of K and V. */

@@ -307,78 +307,120 @@ __device__ __forceinline__ double sum_lanes(double x, int LP) {
   return x;
 }
 
-// Scores of the pages [blockIdx.x * span, + span) of request blockIdx.z for KV
-// head blockIdx.y. LP lanes (a power of two) share a page, 16 bytes of each
+// Scores of `span` pages of request blockIdx.z for KV head blockIdx.x. Heads
+// come first in the order of workgroups, and each request starts at another
+// of its spans, because workgroups go to the 8 dies in turn: with spans first,
+// every short request's only workgroups landed on one die (18 us against 15
+// for 16 ragged requests of up to 64K tokens). LP lanes (a power of two) share a page, 16 bytes of each
 // bound to a lane, so a load instruction covers whole 16 * LP byte rows; each
 // lane keeps its dims' two query sums in fp64. Reading the bounds is what
 // it costs: about 60 vector instructions for 2 KB a wave are a third of the
 // time that HBM takes for them.
+constexpr int kScoreAhead = 4;     // pages per lane whose bounds, and queries, are loaded at a time
+
 template <class T>
 __global__ void __launch_bounds__(kPageThreads) score_kernel(kvtc_pages p, kvtc_requests r, kvtc_queries q, const T* bounds,
                                                              BlockDiv div, kvtc_selection sel, uint32_t* keys, int span, int LP) {
   constexpr int EL = 16 / sizeof(T);
   typedef T row16 __attribute__((ext_vector_type(EL)));
-  const int h = blockIdx.y, i = blockIdx.z, bs = p.block_size, D = p.head_dim, F = p.kv_heads * D;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d0 = (lane & (LP - 1)) * EL;
-  const int len = checked_len(r, bs, i), n = pages_of(len, div), j0 = (int)blockIdx.x * span;
+  const int h = blockIdx.x, i = blockIdx.z, bs = p.block_size, D = p.head_dim, F = p.kv_heads * D;
+  const int lane = threadIdx.x & 63, d0 = (lane & (LP - 1)) * EL;
+  __shared__ __attribute__((aligned(16))) double sums[2][KVTC_MAX_HEAD_DIM];
+  const int j0 = (int)((blockIdx.y + i) % gridDim.y) * span, step = kPageThreads / LP, jl = j0 + (int)threadIdx.x / LP;
+  const int32_t* table = r.block_table + (int64_t)i * r.table_stride;
+  int id[kScoreAhead];
+  auto look_up = [&](int base) {       // (before the length is known: within the table's row all the same)
+#pragma unroll
+    for (int x = 0; x < kScoreAhead; ++x) id[x] = table[min(base + x * step + jl - j0, r.table_width - 1)];
+  };
+  look_up(j0);
+  // a thread sums one dim over the queries; the lanes that need it read it from LDS
+  const int G = q.q_heads / p.kv_heads, dq = (int)threadIdx.x;
+  const T* qh = (const T*)q.q + i * q.q_stride + (int64_t)h * G * D + min(dq, D - 1);
+  T qs[kScoreAhead];
+  auto load_queries = [&](int g) {
+#pragma unroll
+    for (int x = 0; x < kScoreAhead; ++x) qs[x] = qh[(int64_t)min(g + x, G - 1) * D];
+  };
+  load_queries(0);
+  const int len = checked_len(r, bs, i), n = pages_of(len, div);
   if (len < 0 && j0 == 0 && h == 0 && threadIdx.x == 0) set_status(r.status, i, KVTC_E_INVALID);
   if (j0 >= n) return;
   const int j1 = min(n, j0 + span);
   const bool there = d0 < D, all = n <= sel.budget;     // all: every page is selected, whatever its score
-  double up[EL], down[EL];
+  double u = 0.0, w = 0.0;
+  for (int g = 0; g < G && !all; g += kScoreAhead) {
+    if (g) load_queries(g);
 #pragma unroll
-  for (int e = 0; e < EL; ++e) up[e] = down[e] = 0.0;
-  const int G = q.q_heads / p.kv_heads;
-  const T* qh = (const T*)q.q + i * q.q_stride + (int64_t)h * G * D + (there ? d0 : 0);
-  for (int g = 0; g < G && !all; ++g) {
-    const row16 x = *(const row16*)(qh + (int64_t)g * D);
-#pragma unroll
-    for (int e = 0; e < EL; ++e) {
-      const T xe = x[e];
-      const float v = Elem<T>::get(&xe);
-      up[e] += v < 0 ? 0.0 : (double)v;         // (a NaN enters both sums)
-      down[e] += v > 0 ? 0.0 : (double)v;
+    for (int x = 0; x < kScoreAhead; ++x) {
+      const float v = g + x < G ? Elem<T>::get(&qs[x]) : 0.0f;
+      u += (double)(v < 0 ? 0.0f : v);         // (a NaN enters both sums)
+      w += (double)(v > 0 ? 0.0f : v);
     }
   }
-  uint32_t* key = keys + ((int64_t)i * p.kv_heads + h) * r.table_width;
-  const int32_t* table = r.block_table + (int64_t)i * r.table_stride;
-  const int step = kPageThreads / LP;
-  for (int base = j0; base < j1; base += step) {
-    const int j = base + (int)threadIdx.x / LP;
-    const int id = j < j1 ? table[j] : -1;
-    const bool ok = id >= 0 && id < p.n_blocks;
-    const bool keep = all || j < sel.first || j >= n - sel.last;
-    double s0 = 0.0, s1 = 0.0;
-    if (ok && !keep && there) {
-      const T* b = bounds + (int64_t)id * 2 * F + h * D + d0;
-      const row16 lo = *(const row16*)b, hi = *(const row16*)(b + F);
+  if (dq < LP * EL) {       // dims past D: 0
+    sums[0][dq] = dq < D ? u : 0.0;
+    sums[1][dq] = dq < D ? w : 0.0;
+  }
+  __syncthreads();
+  double up[EL], down[EL];
 #pragma unroll
-      for (int e = 0; e < EL; ++e) {
-        const T le = lo[e], he = hi[e];
-        s0 = fma(down[e], (double)Elem<T>::get(&le), s0);
-        s1 = fma(up[e], (double)Elem<T>::get(&he), s1);
+  for (int e = 0; e < EL; ++e) {
+    up[e] = sums[0][d0 + e];
+    down[e] = sums[1][d0 + e];
+  }
+  uint32_t* key = keys + ((int64_t)i * p.kv_heads + h) * r.table_width;
+  for (int base = j0; base < j1; base += kScoreAhead * step) {
+    if (base > j0) look_up(base);
+    row16 lo[kScoreAhead], hi[kScoreAhead];
+    bool ok[kScoreAhead], keep[kScoreAhead];
+#pragma unroll
+    for (int x = 0; x < kScoreAhead; ++x) {
+      const int j = base + x * step + jl - j0;
+      ok[x] = j < j1 && id[x] >= 0 && id[x] < p.n_blocks;
+      keep[x] = all || j < sel.first || j >= n - sel.last;
+      if (ok[x] && !keep[x] && there) {
+        const T* b = bounds + (int64_t)id[x] * 2 * F + h * D + d0;
+        lo[x] = *(const row16*)b;
+        hi[x] = *(const row16*)(b + F);
       }
     }
-    s0 = sum_lanes(s0 + s1, LP);
-    if (j < j1 && (lane & (LP - 1)) == 0) {
-      key[j] = !ok ? 0u : keep ? kKeyKeep : score_key(s0);
-      if (!ok) set_status(r.status, i, KVTC_E_INVALID);
+#pragma unroll
+    for (int x = 0; x < kScoreAhead; ++x) {
+      const int j = base + x * step + jl - j0;
+      double s0 = 0.0, s1 = 0.0;
+      if (ok[x] && !keep[x] && there)
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+          const T le = lo[x][e], he = hi[x][e];
+          s0 = fma(down[e], (double)Elem<T>::get(&le), s0);
+          s1 = fma(up[e], (double)Elem<T>::get(&he), s1);
+        }
+      s0 = sum_lanes(s0 + s1, LP);
+      if (j < j1 && (lane & (LP - 1)) == 0) {
+        key[j] = !ok[x] ? 0u : keep[x] ? kKeyKeep : score_key(s0);
+        if (!ok[x]) set_status(r.status, i, KVTC_E_INVALID);
+      }
     }
   }
 }
 
 // The pages of the highest keys, in ascending order: one workgroup per (KV
-// head, request). The threshold is found by counting digits of kDigit bits,
+// head, request). The threshold is found by counting digits of DIGIT bits,
 // the first over the range that the keys really span, so that they spread
 // over the counters (their leading bits, sign and exponent, hardly differ);
 // each further digit only among the keys that share those before it. A
 // thread has kOwn consecutive keys, in registers for the first kOwn *
-// kPickThreads pages; past them they are read again for every digit.
-constexpr int kPickThreads = 1024, kOwn = 8, kDigit = 11;
+// NT pages; past them they are read again for every digit.
+// NT threads, as many as give each two counters of a digit: 256 where they
+// hold all of a table row's keys, for their barriers are the faster ones.
+constexpr int kOwn = 8;
 
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_requests r, BlockDiv div, kvtc_selection sel, const uint32_t* keys) {
-  constexpr int W = kPickThreads / 64, span = kOwn * kPickThreads;
-  __shared__ uint32_t count[1 << kDigit], part[2 * W], ends[2 * W], found[3];
+template <int NT>
+__global__ void __launch_bounds__(NT) pick_kernel(kvtc_pages p, kvtc_requests r, BlockDiv div, kvtc_selection sel, const uint32_t* keys) {
+  constexpr int W = NT / 64, span = kOwn * NT, DIGIT = NT == 1024 ? 11 : 9;
+  static_assert(2 * NT == 1 << DIGIT, "two counters a thread");
+  __shared__ uint32_t count[1 << DIGIT], part[2 * W], ends[2 * W], found[3];
   const int h = blockIdx.x, i = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = pages_of(checked_len(r, p.block_size, i), div);
   const uint32_t* key = keys + ((int64_t)i * p.kv_heads + h) * r.table_width;
@@ -401,7 +443,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_r
   };
   read(0);
 #pragma unroll
-  for (int x = tid; x < 1 << kDigit; x += kPickThreads) count[x] = 0;
+  for (int x = tid; x < 1 << DIGIT; x += NT) count[x] = 0;
   // Only keys between those that are never taken and those that always are
   // can be the threshold; is there a choice at all?
   uint32_t lo = 0xFFFFFFFFu, hi = 0u, some[2] = {0, 0}, sums[2];      // valid, kept
@@ -431,14 +473,14 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_r
     // want of the keys lo + [0, 2^bits), in which more than that lie
     int bits = 32 - __clz((int)max(hi - lo, 1u));
     for (;;) {
-      const int low = max(bits - kDigit, 0);
+      const int low = max(bits - DIGIT, 0);
       const uint32_t top = hi - lo;
       each([&](uint32_t k) {
         if (k >= lo && k - lo <= top && k != kKeyKeep) atomicAdd(&count[(k - lo) >> low], 1u);
       });
       __syncthreads();
       // from the highest digit down: thread t has digits x + 1 and x
-      const int x = 2 * (kPickThreads - 1 - tid);
+      const int x = 2 * (NT - 1 - tid);
       const uint32_t b = count[x + 1], a = count[x];
       uint32_t above[1] = {a + b}, sum[1];
       scan_threads<W>(above, part, sum);
@@ -484,7 +526,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(kvtc_pages p, kvtc_r
     done += sum[0] & 0xFFFFu;
     tied += sum[0] >> 16;
   }
-  for (uint32_t j = done + min(tied, ties) + tid; j < budget; j += kPickThreads) out[j] = -1;
+  for (uint32_t j = done + min(tied, ties) + tid; j < budget; j += NT) out[j] = -1;
 }
 
 int grid_for(int64_t n, int most) { return (int)std::min<int64_t>(std::max<int64_t>(n, 1), most); }
@@ -533,8 +575,9 @@ void launch_scores(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queri
   // Pages per workgroup: enough workgroups to fill the GPU a few times over
   // where there are as many pages, in whole steps of kPageThreads / lp.
   const int64_t most = (int64_t)r.n_requests * p.kv_heads * r.table_width, step = kPageThreads / lp;
-  const int64_t span = std::min<int64_t>(16, std::max<int64_t>(1, most / (4096 * step))) * step;
-  const dim3 grid((unsigned)((r.table_width + span - 1) / span), p.kv_heads, r.n_requests);
+  const int64_t steps = std::min<int64_t>(16, std::max<int64_t>(1, most / (4096 * step)));
+  const int64_t span = std::max(steps, ((int64_t)r.table_width / step + 65534) / 65535) * step;     // at most 65535 spans
+  const dim3 grid(p.kv_heads, (unsigned)((r.table_width + span - 1) / span), r.n_requests);
   hipLaunchKernelGGL(score_kernel<T>, grid, dim3(kPageThreads), 0, s, p, r, q, (const T*)bounds,
                      block_div(p.block_size), sel, keys, (int)span, lp);
 }
@@ -543,8 +586,11 @@ int launch_page_select(const kvtc_pages& p, const kvtc_requests& r, const kvtc_q
                        const kvtc_selection& sel, void* ws, hipStream_t s) {
   if (p.dtype == KVTC_F32) launch_scores<float>(p, r, q, bounds, sel, (uint32_t*)ws, s);
   else launch_scores<uint16_t>(p, r, q, bounds, sel, (uint32_t*)ws, s);
-  hipLaunchKernelGGL(pick_kernel, dim3(p.kv_heads, r.n_requests), dim3(kPickThreads), 0, s, p, r,
-                     block_div(p.block_size), sel, (const uint32_t*)ws);
+  const dim3 grid(p.kv_heads, r.n_requests);
+  if (r.table_width <= 256 * kOwn)
+    hipLaunchKernelGGL(pick_kernel<256>, grid, dim3(256), 0, s, p, r, block_div(p.block_size), sel, (const uint32_t*)ws);
+  else
+    hipLaunchKernelGGL(pick_kernel<1024>, grid, dim3(1024), 0, s, p, r, block_div(p.block_size), sel, (const uint32_t*)ws);
   return (int)hipGetLastError();
 }
 

@@ -8,6 +8,10 @@ using namespace kvtc;
 
 namespace {
 
+// Tokens of a table row, and entries of all rows: small enough that the
+// kernels' positions a few tiles past an end stay in 32 bits.
+constexpr int64_t kMostEntries = (int64_t)1 << 30;
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 size_t elem_bytes(int dtype) { return dtype == KVTC_F32 ? 4 : 2; }
@@ -71,9 +75,8 @@ kvtc_status check_requests(const kvtc_requests* r, const kvtc_pages& p, bool dat
   if (st != KVTC_OK) return st;
   if (r->table_width <= 0 || r->table_stride < r->table_width)
     return report(KVTC_E_INVALID, "requests: bad table_width or table_stride");
-  if ((int64_t)r->table_width * p.block_size > (int64_t)INT32_MAX ||
-      (int64_t)r->table_width * r->n_requests > (int64_t)INT32_MAX)
-    return report(KVTC_E_UNSUPPORTED, "requests: a table row of 2^31 tokens, or 2^31 table entries, or more");
+  if ((int64_t)r->table_width * p.block_size >= kMostEntries || (int64_t)r->table_width * r->n_requests >= kMostEntries)
+    return report(KVTC_E_UNSUPPORTED, "requests: a table row of 2^30 tokens, or 2^30 table entries, or more");
   if (!data) return KVTC_OK;
   if (!r->block_table || !r->lens || !aligned4(r->block_table) || !aligned4(r->lens) || !aligned4(r->status))
     return report(KVTC_E_INVALID, "requests: block_table and lens must be non-null, all 4-byte aligned");
@@ -140,9 +143,10 @@ kvtc_status kvtc_page_tables(const kvtc_page_plan* a, hipStream_t stream) {
     if (!aligned4(p)) return report(KVTC_E_INVALID, "plan: pointers must be 4-byte aligned");
   if (a->free_from && (a->free_from == a->taken || a->free_from == a->starts))
     return report(KVTC_E_INVALID, "plan: an output overlaps free_from");
-  if ((int64_t)a->n_blocks * a->block_size > (int64_t)INT32_MAX ||
-      (int64_t)a->table_width * a->block_size > (int64_t)INT32_MAX)
+  if ((int64_t)a->n_blocks * a->block_size > (int64_t)INT32_MAX)
     return report(KVTC_E_UNSUPPORTED, "plan: 2^31 rows or more");
+  if ((int64_t)a->table_width * a->block_size >= kMostEntries || (int64_t)a->table_width * a->n_requests >= kMostEntries)
+    return report(KVTC_E_UNSUPPORTED, "plan: a table row of 2^30 tokens, or 2^30 table entries, or more");
   return enqueue(stream, "page tables launch", [&] { return launch_page_tables(*a, stream); });
 }
 

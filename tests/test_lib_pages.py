@@ -59,7 +59,7 @@ BAD_PAGES = [
 BAD_REQUESTS = [
     (INV, dict(block_table=0)), (INV, dict(lens=0)), (INV, dict(lens=P + 2)), (INV, dict(n_requests=0)), (INV, dict(n_requests=-1)),
     (CAP, dict(n_requests=K.KVTC_MAX_JOBS + 1)), (INV, dict(table_width=0)), (INV, dict(table_stride=3)),
-    (UNS, dict(table_width=1 << 27)), (UNS, dict(table_width=1 << 20, n_requests=1 << 12)), (INV, dict(status=P + 1)),
+    (UNS, dict(table_width=1 << 27)), (UNS, dict(table_width=1 << 18, n_requests=1 << 12)), (UNS, dict(table_width=1 << 26)), (INV, dict(status=P + 1)),
 ]
 
 
@@ -133,7 +133,7 @@ def test_null_descriptors_and_buffers():
     (INV, dict(new_lens=0)), (INV, dict(block_table=0)), (INV, dict(free_blocks=0)), (INV, dict(slots=0)), (INV, dict(block_size=0)),
     (INV, dict(n_blocks=0)), (INV, dict(n_free=-1)), (INV, dict(n_slots=-1)), (INV, dict(n_requests=0)),
     (CAP, dict(n_requests=K.KVTC_MAX_JOBS + 1)), (INV, dict(table_width=0)), (INV, dict(table_stride=3)),
-    (UNS, dict(n_blocks=1 << 27)), (UNS, dict(table_width=1 << 27)), (INV, dict(old_lens=P + 1)), (INV, dict(slots=P + 2)),
+    (UNS, dict(n_blocks=1 << 27)), (UNS, dict(table_width=1 << 26)), (UNS, dict(table_width=1 << 18, n_requests=1 << 12)), (INV, dict(old_lens=P + 1)), (INV, dict(slots=P + 2)),
     (INV, dict(free_from=P, taken=P)), (INV, dict(free_from=P, starts=P)),
 ])
 def test_bad_plan(st, kw):
