@@ -353,7 +353,12 @@ __global__ void __launch_bounds__((64 * kWavesOf<T, DP>), (kWavesOf<T, DP> / 4))
   // equal rows then end where ranges do whenever they can, and no range is empty.
   const uint32_t ranges = max(min(gridDim.x, total), 1u), share = total / ranges, rest = total - share * ranges;
   auto start_of = [&](uint32_t w) -> uint32_t { return w * share + w * rest / ranges; };
-  const uint32_t u0 = start_of(min(blockIdx.x, ranges)), u1 = start_of(min(blockIdx.x + 1, ranges));
+  // Workgroups go to the 8 dies in turn. Rows' first ranges go to consecutive
+  // workgroups, then their second ones, and so on, so that the heads of the
+  // same positions, whose pieces lie side by side, are read by different dies.
+  const uint32_t n_rows = n_req * rows_each, turns = gridDim.x / n_rows;
+  const uint32_t wid = blockIdx.x < n_rows * turns ? blockIdx.x % n_rows * turns + blockIdx.x / n_rows : blockIdx.x;
+  const uint32_t u0 = start_of(min(wid, ranges)), u1 = start_of(min(wid + 1, ranges));
   // requests without a token have no chunk
   for (int i = blockIdx.x * NW + wave; i < n_req; i += gridDim.x * NW)
     if (lens[i] == 0) {
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__((64 * kWavesOf<T, DP>), (kWavesOf<T, DP> / 4))
     }
     __syncthreads();
     const bool whole = c0 == 0 && c1 == n;
-    float* part = a.part + (2 * (size_t)blockIdx.x + (c0 ? 0 : 1)) * part_floats(a.gt, DP);
+    float* part = a.part + (2 * (size_t)wid + (c0 ? 0 : 1)) * part_floats(a.gt, DP);
     for (int x = threadIdx.x; x < nq * (DP / 4); x += kThreads) {
       const int qr = x / (DP / 4), d = x % (DP / 4) * 4;
       f32x4 v = {0, 0, 0, 0};
@@ -566,9 +571,9 @@ __global__ void __launch_bounds__((64 * kWavesOf<T, DP>), (kWavesOf<T, DP> / 4))
     }
     // The range starts inside this row's chunks, and their first one lies in the range before: this workgroup's
     // entry tells join_kernel the row and the last range it reaches.
-    if (u == u0 && c0 > 0 && c0 <= u0 - start_of(blockIdx.x - 1)) {
+    if (u == u0 && c0 > 0 && c0 <= u0 - start_of(wid - 1)) {
       const uint32_t tail = u0 - c0 + n - 1;     // the row's last unit
-      uint32_t lo = blockIdx.x, hi = ranges - 1;
+      uint32_t lo = wid, hi = ranges - 1;
       while (lo < hi) {
         const uint32_t mid = (lo + hi + 1) >> 1;
         if (start_of(mid) <= tail) lo = mid;
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__((64 * kWavesOf<T, DP>), (kWavesOf<T, DP> / 4))
     __syncthreads();
     u += end - off;
   }
-  if (threadIdx.x == 0) a.meta[blockIdx.x] = meta;
+  if (threadIdx.x == 0) a.meta[wid] = meta;
 }
 
 // Adds the pieces of one row and query head: workgroup (w, query) does so if
