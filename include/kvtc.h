@@ -462,8 +462,9 @@ kvtc_status kvtc_lossless_sizes(const void* d_ws, int32_t n_jobs, uint64_t* size
  * Pages of KVTC_BF16 or KVTC_F32; any block_size; head_dim a multiple of 8
  * up to KVTC_MAX_HEAD_DIM; fewer than 2^31 rows in the pages, 2^30 tokens in
  * a table row and 2^30 entries in all table rows; at most KVTC_MAX_JOBS
- * requests per call. Requests may share pages. Page, bounds, q and out pointers are
- * 16-byte aligned, strides count elements and are multiples of 8.
+ * requests per call. Requests may share pages. Page, bounds, q and out
+ * pointers are 16-byte aligned; strides count elements, those of q and out
+ * multiples of 8.
  * ---------------------------------------------------------------------- */
 
 /* Largest head_dim the paged calls take. */
@@ -557,8 +558,8 @@ typedef struct {
 
 /* Write row i of rows->k and rows->v to row slots[i] of the pages, converted
  * to the pages' type (round to nearest even) where it differs. A row with a
- * slot below 0 is skipped; one with a slot past the pages too, with status
- * KVTC_E_INVALID. Slots are distinct: of two rows with one slot, each element
+ * slot below 0 may be read and is not written; nor is one with a slot past
+ * the pages, with status KVTC_E_INVALID. Slots are distinct: of two rows with one slot, each element
  * comes from either. The rows may be any element-aligned view (a slice of a
  * fused projection, say); they go in 16-byte pieces where rows, strides and F
  * allow. */

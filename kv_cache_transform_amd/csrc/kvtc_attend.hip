@@ -2,18 +2,20 @@
 //
 // For each (request, KV head), G query heads share the keys and values:
 // s = scale K q, p = exp(s - max), out = p V / sum p. Every key and value is
-// read once, for 2 G / element bytes operations a byte, so HBM bounds it.
+// read once, for 2 G / element bytes operations a byte, so HBM bounds it:
+// 6.6 TB/s over eight requests of 64K tokens (8 heads of 128, bf16, 325 us),
+// where a copy of the reads alone reaches 6.3 to 6.9 by its order of rows.
+// Short work is bound by its chain: lengths, pages, rows, join (14 us for one
+// request of 8K tokens, 6 of which HBM needs).
 //
-// attend_kernel: a fixed number of workgroups each take an equal range of the
-// work, counted in chunks of kAttChunk positions of one row (request, KV head,
-// 16 query heads); the ranges follow from the lengths on the device, so ragged
-// batches stay balanced and a captured graph follows new lengths. Inside a
-// chunk each wave has a tile of positions of its own, loads K and V straight
-// into the registers the matrix instructions read (nothing is shared between
-// waves, so LDS would only add a copy), and keeps its own running maximum and
-// sums; the waves join in LDS at the end of a row's piece. A row that lies in
-// one range is finished there, pieces of the others go to the workspace and
-// join_kernel adds them in a fixed order.
+// attend_kernel: one workgroup per CU takes an equal share of the work, counted
+// in chunks of positions of one row (request, KV head, 16 query heads); the
+// shares follow from the lengths on the device, so ragged batches stay balanced
+// and a captured graph follows new lengths. Inside a chunk each wave has a tile
+// of positions of its own and keeps its own running maximum and sums; the
+// waves join in LDS at the end of a row's piece. A row that lies in one share
+// is finished there, pieces of the others go to the workspace and join_kernel
+// adds them in a fixed order (4 us, most of it the second launch).
 #include "kvtc_pages_device.h"
 
 namespace kvtc {
@@ -289,17 +291,15 @@ __device__ __forceinline__ float sum_groups(float x) {
 // page a tile, its group's, and not one for each of its rows.
 //
 // The next tile's keys are loaded as soon as this one's scores are computed,
-// its values after the second product, so one set of registers and one buffer
-// a wave keep loads in flight and leave room for more waves. Lookups run ahead
-// by a tile for each load in their chain, and are only looked at when they
-// are needed: a wait for one would be a wait for all data loaded before it.
-// (Without whole groups there are too many to hold; they are waited for.)
-template <class T, int DP>
-constexpr int kWavesOf = attend_waves(sizeof(T) == 4 ? KVTC_F32 : KVTC_BF16, DP);
-
+// its values after the second product: 16 KB a wave in flight at head_dim 128
+// (a second buffer of keys changed nothing: 339 us against 338 over 8 x 64K
+// tokens). Lookups run ahead by a tile for each load in their chain, and are
+// only looked at when they are needed: a wait for one would be a wait for all
+// data loaded before it. (Without whole groups there are too many to hold;
+// they are waited for: 4.2 TB/s with pages of 20 against 6.3 with 16.)
 template <class T, int DP, bool GROUPED>
-__global__ void __launch_bounds__((64 * kWavesOf<T, DP>), (kWavesOf<T, DP> / 4)) attend_kernel(AttendArgs a) {
-  constexpr int NW = kWavesOf<T, DP>, kThreads = 64 * NW;
+__global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(AttendArgs a) {
+  constexpr int NW = kAttendWaves, kThreads = 64 * NW;
   typedef Tile<T, DP> TT;
   typedef Keys<T, DP> KK;
   constexpr int TK = TT::TK, TG = TT::TG, CH = NW * TK, NS = TK / 4;
@@ -320,7 +320,8 @@ __global__ void __launch_bounds__((64 * kWavesOf<T, DP>), (kWavesOf<T, DP> / 4))
   // positions of a request: its tokens, or those of as many selected pages as it has pages
   auto positions = [&](int len) -> int { return a.sel.blocks ? min(a.sel.budget, pages_of(len, a.div)) * bs : len; };
   // A row counts as its chunks, and one that a range holds with others as
-  // kAttendRow more: so much longer its start and end take.
+  // kAttendRow more: so much longer its start and end take (128 ragged
+  // requests of up to 16K tokens: 269 us without, 159 with).
   uint32_t total, range;
   auto extra = [&](uint32_t n) -> uint32_t { return n < range ? kAttendRow : 0u; };
   {
@@ -355,7 +356,8 @@ __global__ void __launch_bounds__((64 * kWavesOf<T, DP>), (kWavesOf<T, DP> / 4))
   auto start_of = [&](uint32_t w) -> uint32_t { return w * share + w * rest / ranges; };
   // Workgroups go to the 8 dies in turn. Rows' first ranges go to consecutive
   // workgroups, then their second ones, and so on, so that the heads of the
-  // same positions, whose pieces lie side by side, are read by different dies.
+  // same positions, whose pieces lie side by side, are read by different dies
+  // (8 x 64K tokens: 337 us in plain order, 325 so).
   const uint32_t n_rows = n_req * rows_each, turns = gridDim.x / n_rows;
   const uint32_t wid = blockIdx.x < n_rows * turns ? blockIdx.x % n_rows * turns + blockIdx.x / n_rows : blockIdx.x;
   const uint32_t u0 = start_of(min(wid, ranges)), u1 = start_of(min(wid + 1, ranges));
@@ -660,9 +662,9 @@ __global__ void __launch_bounds__(kPageThreads) join_kernel(AttendArgs a) {
 
 template <class T, int DP, bool GROUPED>
 void launch_pieces(const AttendArgs& a, uint32_t grid, hipStream_t s) {
-  const size_t lds = (size_t)kWavesOf<T, DP> * Keys<T, DP>::BYTES + (size_t)a.r.n_requests * 8;
+  const size_t lds = (size_t)kAttendWaves * Keys<T, DP>::BYTES + (size_t)a.r.n_requests * 8;
   allow_lds(attend_kernel<T, DP, GROUPED>, lds + 1024);      // with what the kernel declares itself
-  hipLaunchKernelGGL((attend_kernel<T, DP, GROUPED>), dim3(grid), dim3(64 * kWavesOf<T, DP>), lds, s, a);
+  hipLaunchKernelGGL((attend_kernel<T, DP, GROUPED>), dim3(grid), dim3(64 * kAttendWaves), lds, s, a);
 }
 
 template <class T, int DP>

@@ -1,6 +1,7 @@
 // Host side of the paged-cache calls: argument checks, sizes and launches.
 // Nothing here allocates or throws apart from the error message.
 #include <cmath>
+#include <cstdio>
 
 #include "kvtc_pages.h"
 
@@ -37,8 +38,9 @@ kvtc_status enqueue(hipStream_t s, const char* what, L launch) {
   OnDeviceOf guard(s);
   const int e = launch();
   if (e == 0) return KVTC_OK;
-  (void)what;
-  return report(KVTC_E_HIP, hipGetErrorString((hipError_t)e));
+  char msg[160];
+  std::snprintf(msg, sizeof(msg), "%s: %s", what, hipGetErrorString((hipError_t)e));
+  return report(KVTC_E_HIP, msg);
 }
 
 size_t row_elems(const kvtc_pages& p) { return (size_t)p.kv_heads * p.head_dim; }

@@ -123,17 +123,18 @@ def test_attend(i):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("lens", [[9000], [5000, 1, 0, 3], [40, 6000, 40, 2500, 1]])
+@pytest.mark.parametrize("lens", [[9000], [5000, 1, 0, 3], [40, 6000, 40, 2500, 1], [300] * 37, [129, 128, 1] * 30, [20000]])
 def test_attend_long_lengths_are_split_and_joined(dtype, lens):
     c = case(5, dtype, 2, 4, 64, 16, lens)
     out, lse, st = attend(c, 0.125)
     check_attend(c, 0.125, out, lse, status=st)
 
 
-def test_attend_many_requests():
+@pytest.mark.parametrize("n", [700, 4096])
+def test_attend_many_requests(n):
     r = np.random.default_rng(8)
-    lens = [int(x) for x in r.integers(0, 90, 700)]
-    c = case(9, BF16, 2, 2, 64, 16, lens)
+    lens = [int(x) for x in r.integers(0, 90, n)]
+    c = case(9, BF16, 1, 2, 64, 16, lens)
     out, lse, st = attend(c, 0.125)
     check_attend(c, 0.125, out, lse, status=st)
 
@@ -152,6 +153,24 @@ def test_attend_never_uses_stale_rows(dtype, stale):
     c = case(12, dtype, 2, 4, 128, 16, [1, 15, 17, 100, 0], stale=stale)
     out, lse, st = attend(c, 0.1)
     check_attend(c, 0.1, out, lse, status=st)
+
+
+def test_attend_writes_where_it_reads():
+    """out may take the place of q: a row's queries are read before any of its results are written."""
+    c = case(50, BF16, 2, 4, 64, 16, [3000, 1, 40, 0])
+    ref, lse, _ = attend(c, 0.125)
+    buf = c["q"].reshape(4, 512).clone()
+    out, lse2, _ = attend(c, 0.125, q=buf, out=buf)
+    assert torch.equal(out, ref) and torch.equal(lse, lse2)
+
+
+def test_attend_requests_that_share_pages():
+    c = case(51, F32, 2, 2, 64, 16, [200, 100, 64])
+    c["table"][1, :7] = c["table"][0, :7]
+    c["table"][2, :3] = c["table"][0, 2:5]
+    c["dtable"].copy_(dev(c["table"]))
+    out, lse, st = attend(c, 0.125)
+    check_attend(c, 0.125, out, lse, status=st)
 
 
 def test_attend_strided_rows_and_what_lies_beside_them():
