@@ -625,7 +625,7 @@ kvtc_status kvtc_page_select(const kvtc_pages* pages, const kvtc_requests* reque
  * over the tokens t < lens[i], or with a selection over those of them in the
  * selected pages (of a request with m pages the first min(budget, m) entries
  * are read; entries below 0 or past its pages are left out, a page listed
- * twice counts twice). No tokens: out = 0 and lse = -inf. Rows of
+ * twice counts twice). out may take the place of q. No tokens: out = 0 and lse = -inf. Rows of
  * a page behind lens[i] are never used, whatever they hold. Sums and the
  * softmax's maximum and sum are fp32; out is rounded once. Equal calls give
  * equal bits. */
