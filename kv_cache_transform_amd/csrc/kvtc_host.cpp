@@ -17,6 +17,7 @@
 
 #include "kvtc_internal.h"
 #include "kvtc_linalg.h"
+#include "kvtc_pages.h"
 
 using namespace kvtc;
 

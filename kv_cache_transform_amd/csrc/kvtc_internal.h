@@ -301,9 +301,6 @@ struct LzArgs {
   unsigned long long* sizes;              // container bytes per job (encode)
 };
 
-// Set kvtc_last_error's message of this thread and return st (kvtc_host.cpp).
-kvtc_status report(kvtc_status st, const char* msg);
-
 // Host-side launchers implemented in kvtc_encode.hip and kvtc_decode.hip (G = group size, lds =
 // dynamic LDS bytes). Every job of one launch has the same shape parameter:
 // nb = r_enc / 32 for encode, ks = r_dec / 16 for the decode stages. They

@@ -7,6 +7,9 @@
 
 namespace kvtc {
 
+// Set kvtc_last_error's message of this thread and return st (kvtc_host.cpp).
+kvtc_status report(kvtc_status st, const char* msg);
+
 constexpr int kPageThreads = 256;
 
 // Scores of kvtc_page_select: one ordered 32-bit key per (request, KV head,
