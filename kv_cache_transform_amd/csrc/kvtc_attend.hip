@@ -79,17 +79,28 @@ struct Keys {
     const int d = place(at(x, l), l % CPR) * EL;
     return d < D ? d : 0;
   }
-  // Rows of whole groups: an instruction's rows lie in one group, whose first
-  // row is group(y), the same for all lanes; `row` bytes apart.
-  template <class Group>
-  __device__ __forceinline__ static void load_groups(uint8_t* buf, Group group, int row, int D, int l) {
+  __device__ __forceinline__ static void copy(uint8_t* to, const T* rows, int row, int offset) {
+    const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc((void*)rows, 0, TG * row, 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, offset, 0, 0, kNt);
+  }
+  // Rows `row` bytes apart, and an instruction's rows lie in one group y: its
+  // first `split(y)` rows from first(y) on, the others from second(y) on, each
+  // the same for all lanes. Lanes on the other side of a split sit out.
+  template <bool TWO, class First, class Second, class Split>
+  __device__ __forceinline__ static void load_groups(uint8_t* buf, First first, Second second, Split split, int row, int D, int l) {
     static_assert(RPI <= TG, "one group an instruction");
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int x = 0; x < NX; ++x) {
-      const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc((void*)group(x * RPI / TG), 0, TG * row, 0x00027000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rows, (__attribute__((address_space(3))) void*)(buf + 1024 * x), 16,
-                                               (l / CPR) * row + elem(x, l, D) * (int)sizeof(T), (x * RPI % TG) * row, 0, kNt);
+      const int y = x * RPI / TG, pos = at(x, l) % TG, in = elem(x, l, D) * (int)sizeof(T);
+      uint8_t* to = buf + 1024 * x;
+      if (!TWO || split(y) >= TG) {
+        copy(to, first(y), row, pos * row + in);
+      } else if (pos < split(y)) {
+        copy(to, first(y), row, pos * row + in);
+      } else {
+        copy(to, second(y), row, (pos - split(y)) * row + in);
+      }
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -286,24 +297,26 @@ __device__ __forceinline__ float sum_groups(float x) {
   return x + __shfl_xor(x, 32, 64);
 }
 
-// DP: head_dim rounded up to 64, 128 or 256. GROUPED: every page holds whole
-// groups of TG positions (block_size is a multiple), so a lane looks up one
-// page a tile, its group's, and not one for each of its rows.
+// DP: head_dim rounded up to 64, 128 or 256. PAGES: in how many pages the TG
+// positions of a group can lie, so how many a lane looks up a tile: 1 where
+// block_size is a multiple of TG, 2 where it is larger; 0 for smaller pages,
+// where a lane looks up each of its rows (8 x 16K tokens, bf16: 89 us with
+// pages of 16, 94 with pages of 20, 127 with those taken row by row).
 //
 // The next tile's keys are loaded as soon as this one's scores are computed,
 // its values after the second product: 16 KB a wave in flight at head_dim 128
 // (a second buffer of keys changed nothing: 339 us against 338 over 8 x 64K
 // tokens). Lookups run ahead by a tile for each load in their chain, and are
 // only looked at when they are needed: a wait for one would be a wait for all
-// data loaded before it. (Without whole groups there are too many to hold;
-// they are waited for: 4.2 TB/s with pages of 20 against 6.3 with 16.)
-template <class T, int DP, bool GROUPED>
+// data loaded before it. (At PAGES = 0 there are too many to hold; they are
+// waited for.)
+template <class T, int DP, int PAGES>
 __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(AttendArgs a) {
   constexpr int NW = kAttendWaves, kThreads = 64 * NW;
   typedef Tile<T, DP> TT;
   typedef Keys<T, DP> KK;
   constexpr int TK = TT::TK, TG = TT::TG, CH = NW * TK, NS = TK / 4;
-  constexpr int NL = GROUPED ? 1 : TG + KK::NX;       // lookups of a lane: its group, or its value rows and its key rows
+  constexpr int NL = PAGES ? PAGES : TG + KK::NX;       // lookups of a lane: its group's pages, or its value rows and its key rows
   constexpr uint32_t kFull = (1u << TG) - 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ uint32_t scan_part[NW];
@@ -392,9 +405,14 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(AttendArgs a)
     // A position's page, in steps between which a load is on its way: the entry
     // of the table (from the list, or the page's index), the entry's page, and
     // from that the position's row and the number of tokens from there on.
+    auto first_of = [&](uint32_t ch) -> int { return (int)ch * CH + wave * TK + TG * g; };      // of the lane's group
+    auto split_of = [&](uint32_t ch) -> int {      // how many of its positions lie in its first page
+      const int pos = first_of(ch);
+      return pos < n_pos ? min(bs - (pos - (int)div_block(pos, a.div) * bs), TG) : TG;
+    };
     auto pos_of = [&](uint32_t ch, int x) -> int {
-      const int P = (int)ch * CH + wave * TK;
-      return x < TG ? P + TG * g + x : P + KK::at(x - TG, lane);
+      if constexpr (PAGES > 0) return first_of(ch) + (x ? min(split_of(ch), TG - 1) : 0);
+      else return x < TG ? first_of(ch) + x : (int)ch * CH + wave * TK + KK::at(x - TG, lane);
     };
     auto entry_of = [&](uint32_t ch, int x) -> int {
       const int slot = (int)div_block(min(pos_of(ch, x), n_pos - 1), a.div);
@@ -414,31 +432,39 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(AttendArgs a)
       return id * bs + off;
     };
     TT t;
-    int row_at[NL];
+    int row_at[NL], split = TG;
     uint32_t live = 0;
     // rows of a tile's positions, and which positions of the lane's group are attended to
     auto resolve = [&](uint32_t ch, const int* entry, const int* id) -> uint32_t {
       uint32_t bits = 0;
+      if constexpr (PAGES == 2) split = split_of(ch);
 #pragma unroll
       for (int x = 0; x < NL; ++x) {
         int left;
         row_at[x] = row_of(ch, x, entry[x], id[x], &left);
-        if (GROUPED) bits = left >= TG ? kFull : (1u << left) - 1;
-        else if (x < TG) bits |= left > 0 ? 1u << x : 0u;
+        if constexpr (PAGES > 0) {
+          const int from = x ? split : 0, there = min(left, x ? TG - split : split);
+          bits |= ((1u << there) - 1) << from;
+        } else if (x < TG) {
+          bits |= left > 0 ? 1u << x : 0u;
+        }
       }
       return bits;
     };
     auto load_keys = [&]() {
-      if constexpr (GROUPED)
-        KK::load_groups(keys, [&](int y) { return kh + (int64_t)__builtin_amdgcn_readlane(row_at[0], 16 * y) * F; },
-                        (int)(F * sizeof(T)), D, lane);
+      if constexpr (PAGES > 0)
+        KK::template load_groups<PAGES == 2>(
+            keys, [&](int y) { return kh + (int64_t)__builtin_amdgcn_readlane(row_at[0], 16 * y) * F; },
+            [&](int y) { return kh + (int64_t)__builtin_amdgcn_readlane(row_at[PAGES - 1], 16 * y) * F; },
+            [&](int y) { return __builtin_amdgcn_readlane(split, 16 * y); }, (int)(F * sizeof(T)), D, lane);
       else
         KK::load_rows(keys, [&](int x) { return kh + (int64_t)row_at[TG + x] * F; }, D, lane);
     };
     auto load_values = [&]() {
-      if constexpr (GROUPED) {
+      if constexpr (PAGES > 0) {
         const T* first = vh + (int64_t)row_at[0] * F;
-        t.load_values([&](int e) { return first + e * F; }, D, r);
+        const T* second = vh + (int64_t)row_at[PAGES - 1] * F;
+        t.load_values([&](int e) { return PAGES == 1 || e < split ? first + e * F : second + (e - split) * F; }, D, r);
       } else {
         t.load_values([&](int e) { return vh + (int64_t)row_at[e] * F; }, D, r);
       }
@@ -448,8 +474,8 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(AttendArgs a)
     float m = -INFINITY, l = 0.0f;
     f32x4 o[TT::OUT];
 
-    // of the next tile, and of the one after (GROUPED)
-    int entry[NL], id[NL], entry2 = 0;
+    // of the next tile, and (PAGES > 0) of the one after
+    int entry[NL], id[NL], entry2[NL];
     auto look_up = [&](uint32_t ch) {
 #pragma unroll
       for (int x = 0; x < NL; ++x) entry[x] = entry_of(ch, x);
@@ -460,16 +486,18 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(AttendArgs a)
     auto tile = [&](uint32_t ch, auto more) {
       uint32_t live_next = 0;
       if constexpr (more) {
-        if constexpr (!GROUPED) look_up(ch + 1);
+        if constexpr (PAGES == 0) look_up(ch + 1);
         live_next = resolve(ch + 1, entry, id);
-        if constexpr (GROUPED) {
-          entry[0] = entry2;
-          id[0] = page_of(entry2);
-          entry2 = entry_of(ch + 3, 0);
+#pragma unroll
+        for (int x = 0; x < PAGES; ++x) {
+          entry[x] = entry2[x];
+          id[x] = page_of(entry2[x]);
         }
+#pragma unroll
+        for (int x = 0; x < PAGES; ++x) entry2[x] = entry_of(ch + 3, x);
       }
       float s[NS];
-      KK::template landed<TG * TT::VB + (more && GROUPED ? 1 : 0)>();
+      KK::template landed<TG * TT::VB + (more && PAGES == 1 ? 1 : 0)>();     // loads that follow the keys: values, a page at least
       TT::scores(q, keys, s, D, g, r);
       if constexpr (more) load_keys();
 #pragma unroll
@@ -508,10 +536,11 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(AttendArgs a)
 #pragma unroll
     for (int j = 0; j < TT::OUT; ++j) o[j] = f32x4{0, 0, 0, 0};
     live = resolve(c0, entry, id);
-    if constexpr (GROUPED) {
-      entry[0] = entry_of(c0 + 1, 0);
-      entry2 = entry_of(c0 + 2, 0);
-      id[0] = page_of(entry[0]);
+#pragma unroll
+    for (int x = 0; x < PAGES; ++x) {
+      entry[x] = entry_of(c0 + 1, x);
+      entry2[x] = entry_of(c0 + 2, x);
+      id[x] = page_of(entry[x]);
     }
     load_keys();
     load_values();
@@ -660,17 +689,19 @@ __global__ void __launch_bounds__(kPageThreads) join_kernel(AttendArgs a) {
     a.q.lse[(int64_t)i * a.q.q_heads + hq] = sum == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-template <class T, int DP, bool GROUPED>
+template <class T, int DP, int PAGES>
 void launch_pieces(const AttendArgs& a, uint32_t grid, hipStream_t s) {
   const size_t lds = (size_t)kAttendWaves * Keys<T, DP>::BYTES + (size_t)a.r.n_requests * 8;
-  allow_lds(attend_kernel<T, DP, GROUPED>, lds + 1024);      // with what the kernel declares itself
-  hipLaunchKernelGGL((attend_kernel<T, DP, GROUPED>), dim3(grid), dim3(64 * kAttendWaves), lds, s, a);
+  allow_lds(attend_kernel<T, DP, PAGES>, lds + 1024);      // with what the kernel declares itself
+  hipLaunchKernelGGL((attend_kernel<T, DP, PAGES>), dim3(grid), dim3(64 * kAttendWaves), lds, s, a);
 }
 
 template <class T, int DP>
 int launch(const AttendArgs& a, uint32_t grid, hipStream_t s) {
-  if (a.p.block_size % Tile<T, DP>::TG == 0) launch_pieces<T, DP, true>(a, grid, s);
-  else launch_pieces<T, DP, false>(a, grid, s);
+  constexpr int TG = Tile<T, DP>::TG;
+  if (a.p.block_size % TG == 0) launch_pieces<T, DP, 1>(a, grid, s);
+  else if (a.p.block_size > TG) launch_pieces<T, DP, 2>(a, grid, s);
+  else launch_pieces<T, DP, 0>(a, grid, s);
   if (grid > 1)
     hipLaunchKernelGGL((join_kernel<T, DP>), dim3(grid, a.gt), dim3(kPageThreads), 0, s, a);
   return (int)hipGetLastError();

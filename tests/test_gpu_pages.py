@@ -109,6 +109,10 @@ ATTEND = [
     (F32, 2, 16, 80, 20, [333, 20, 19, 21]), (BF16, 1, 17, 96, 8, [130, 8, 4]), (F32, 1, 17, 96, 8, [130, 8, 4]),
     (BF16, 1, 40, 128, 64, [500, 64, 1]), (BF16, 2, 8, 192, 32, [257, 31]), (F32, 2, 8, 192, 32, [257, 31]),
     (BF16, 2, 5, 256, 16, [400, 17]), (F32, 2, 5, 256, 16, [400, 17]), (BF16, 2, 2, 200, 24, [100, 25]),
+    # pages that cut the kernels' groups of 8 or 4 positions, and pages smaller than a group
+    (BF16, 2, 4, 128, 9, [1, 8, 9, 10, 17, 18, 19, 300, 0]), (BF16, 1, 4, 64, 11, [260, 11, 10, 12, 1]), (BF16, 2, 3, 256, 12, [130, 13, 12]),
+    (BF16, 2, 16, 128, 15, [600, 14, 15, 16]), (F32, 2, 3, 128, 5, [200, 4, 5, 6, 1]), (F32, 1, 2, 256, 6, [90, 7, 0]),
+    (F32, 3, 4, 64, 9, [300, 8, 9, 10]), (BF16, 2, 4, 128, 7, [300, 6, 7, 8]), (F32, 2, 4, 64, 3, [100, 2, 3, 4]), (F32, 2, 4, 128, 2, [70]),
     (BF16, 1, 4, 128, 100, [1, 99, 100, 101, 950]), (BF16, 4, 2, 40, 5, [77, 4, 5, 6]), (F32, 4, 2, 24, 7, [77, 6, 7, 8]),
 ]
 
@@ -148,9 +152,10 @@ def test_attend_scales(dtype, scale, gain):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bs", [16, 12, 9, 6, 3])
 @pytest.mark.parametrize("stale", [NAN, float("inf"), float("-inf"), 3.0e38])
-def test_attend_never_uses_stale_rows(dtype, stale):
-    c = case(12, dtype, 2, 4, 128, 16, [1, 15, 17, 100, 0], stale=stale)
+def test_attend_never_uses_stale_rows(dtype, bs, stale):
+    c = case(12, dtype, 2, 4, 128, bs, [1, 15, 17, 100, 0], stale=stale)
     out, lse, st = attend(c, 0.1)
     check_attend(c, 0.1, out, lse, status=st)
 
@@ -195,11 +200,12 @@ def test_attend_without_lse_and_status():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_attend_leaves_out_bad_pages_and_lengths(dtype):
-    c = case(15, dtype, 2, 4, 64, 16, [40, 100, 64, 10, 33])
+@pytest.mark.parametrize("bs", [16, 13, 5])
+def test_attend_leaves_out_bad_pages_and_lengths(dtype, bs):
+    c = case(15, dtype, 2, 4, 64, bs, [40, 100, 64, 10, 33])
     c["table"][1, 2], c["table"][2, 0], c["table"][2, 3], c["table"][3, 0] = -1, c["n_blocks"], -2**31, 2**31 - 1
     c["dtable"].copy_(dev(c["table"]))
-    c["lens"] = np.array([40, 100, 64, 10, c["width"] * 16 + 1])
+    c["lens"] = np.array([40, 100, 64, 10, c["width"] * bs + 1])
     c["dlens"].copy_(dev(c["lens"]))
     out, lse, st = attend(c, 0.125)
     check_attend(c, 0.125, out, lse, status=st)
@@ -213,7 +219,8 @@ def test_attend_leaves_out_bad_pages_and_lengths(dtype):
     assert list(attend(c, 0.125)[2]) == [-3, -1, -1, -1, -1]
 
 
-@pytest.mark.parametrize("dtype,heads,group,dim,bs", [(BF16, 2, 4, 128, 16), (F32, 2, 4, 64, 16), (BF16, 3, 5, 80, 5), (BF16, 1, 20, 64, 32)])
+@pytest.mark.parametrize("dtype,heads,group,dim,bs", [(BF16, 2, 4, 128, 16), (F32, 2, 4, 64, 16), (BF16, 3, 5, 80, 5), (BF16, 1, 20, 64, 32),
+                                                       (BF16, 2, 4, 128, 12), (F32, 1, 4, 64, 6), (BF16, 2, 4, 64, 9), (F32, 2, 2, 128, 3)])
 def test_attend_over_selected_pages(dtype, heads, group, dim, bs):
     lens = [0, 1, bs, 5 * bs - 1, 40 * bs + 1]
     c = case(16, dtype, heads, group, dim, bs, lens)
