@@ -311,11 +311,12 @@ __device__ __forceinline__ double sum_lanes(double x, int LP) {
 // come first in the order of workgroups, and each request starts at another
 // of its spans, because workgroups go to the 8 dies in turn: with spans first,
 // every short request's only workgroups landed on one die (18 us against 15
-// for 16 ragged requests of up to 64K tokens). LP lanes (a power of two) share a page, 16 bytes of each
-// bound to a lane, so a load instruction covers whole 16 * LP byte rows; each
-// lane keeps its dims' two query sums in fp64. Reading the bounds is what
-// it costs: about 60 vector instructions for 2 KB a wave are a third of the
-// time that HBM takes for them.
+// for 16 ragged requests of up to 64K tokens). LP lanes (a power of two) share
+// a page, 16 bytes of each bound to a lane, so a load instruction covers whole
+// 16 * LP byte rows; the query sums, a dim a thread, come from LDS. Reading
+// the bounds is what it costs (134 MB of 32 x 1024 pages of 8 heads in 37 us);
+// the sums in fp64, which make the choice independent of their order, are a
+// fifth of it (30 us without).
 constexpr int kScoreAhead = 4;     // pages per lane whose bounds, and queries, are loaded at a time
 
 template <class T>

@@ -593,6 +593,35 @@ def test_two_streams_at_once():
         assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+def test_two_graphs_share_a_workspace():
+    """Two captured batches of different sizes on one workspace, replayed in turn with eager work between."""
+    cs = [case(60, BF16, 2, 4, 128, 16, [4000, 3, 0, 700]), case(61, BF16, 1, 7, 64, 20, [90, 2500])]
+    want, outs, calls = [], [], []
+    for c in cs:
+        n, hq = len(c["lens"]), c["heads"] * c["group"]
+        want.append(attend(c, 0.1)[:2])
+        out = torch.zeros((n, hq * c["dim"]), dtype=torch.bfloat16, device=DEV)
+        lse = torch.zeros((n, hq), device=DEV)
+        outs.append((out, lse))
+        calls.append((c, K.make_queries(c["q"], out, hq, 0.1, lse=lse)))
+    ws = torch.full((max(K.kvtc_page_workspace_bytes(c["pages"], c["req"], q) for c, q in calls),), 0xA5, dtype=torch.uint8, device=DEV)
+    graphs = []
+    side = torch.cuda.Stream()
+    for c, q in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            K.kvtc_page_attend(c["pages"], c["req"], q, None, ws, stream=side)
+        graphs.append(g)
+    for i in (0, 1, 0, 0, 1, 1, 0):
+        for x in outs[i]:
+            x.zero_()
+        graphs[i].replay()
+        if i:
+            ws.random_()              # eager work that leaves other contents
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+
+
 def step_buffers(n, heads, group, dim, bs, n_blocks, width, budget, dtype):
     F, hq = heads * dim, heads * group
     z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device=DEV)  # noqa: E731
