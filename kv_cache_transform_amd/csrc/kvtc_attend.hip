@@ -38,10 +38,6 @@ struct AttendArgs {
   uint4* meta;          // per workgroup: the row that its range starts inside (see join_kernel)
 };
 
-// A piece of a row in the workspace: gt rows of DP sums, gt maxima (base 2),
-// gt sums of weights.
-__host__ __device__ constexpr size_t part_floats(int gt, int dp) { return (size_t)gt * (dp + 2); }
-
 // One wave's tile: positions [P, P + TK) of a row, in TK / TG = 4 groups of TG.
 // Lane l = 16 g + r.
 //

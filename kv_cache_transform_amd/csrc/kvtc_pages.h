@@ -37,13 +37,15 @@ inline uint32_t attend_workers(const kvtc_pages& p, const kvtc_requests& r, cons
   const int64_t n = attend_most_chunks(p, r, q);
   return (uint32_t)(n < kAttendWorkers ? n : kAttendWorkers);
 }
-// Workspace: an entry per workgroup, then two pieces of rows per workgroup
-// (up to 16 query heads' sums, maxima and weights).
+// Workspace: an entry per workgroup, then two pieces of rows per workgroup: gt
+// (up to 16) query heads' dp sums each, their gt maxima (base 2) and their gt
+// sums of weights, in whole 16 bytes.
+__host__ __device__ constexpr size_t part_floats(int gt, int dp) { return ((size_t)gt * (dp + 2) + 3) / 4 * 4; }
 inline size_t attend_meta_bytes() { return align_up((size_t)kAttendWorkers * 16, kAlign); }
 inline size_t attend_ws_bytes(const kvtc_pages& p, const kvtc_requests& r, const kvtc_queries& q) {
   const int group = q.q_heads / p.kv_heads, gt = group < 16 ? group : 16;
   return attend_meta_bytes() +
-         align_up((size_t)attend_workers(p, r, q) * 2 * gt * (attend_dp(p.head_dim) + 2) * 4, kAlign);
+         align_up(attend_workers(p, r, q) * 2 * part_floats(gt, attend_dp(p.head_dim)) * 4, kAlign);
 }
 
 // Every launcher returns a hipError_t value cast to int.
