@@ -559,10 +559,10 @@ typedef struct {
 /* Write row i of rows->k and rows->v to row slots[i] of the pages, converted
  * to the pages' type (round to nearest even) where it differs. A row with a
  * slot below 0 may be read and is not written; nor is one with a slot past
- * the pages, with status KVTC_E_INVALID. Slots are distinct: of two rows with one slot, each element
- * comes from either. The rows may be any element-aligned view (a slice of a
- * fused projection, say); they go in 16-byte pieces where rows, strides and F
- * allow. */
+ * the pages, with status KVTC_E_INVALID. Slots are distinct: of two rows with
+ * one slot, each element comes from either. The rows may be any element-aligned
+ * view (a slice of a fused projection, say); they go in 16-byte pieces where
+ * rows and strides allow. */
 kvtc_status kvtc_page_write(const kvtc_pages* pages, const kvtc_page_rows* rows, hipStream_t stream);
 
 /* Key bounds of the pages that hold tokens [from_lens[i], lens[i]) of request
@@ -625,10 +625,10 @@ kvtc_status kvtc_page_select(const kvtc_pages* pages, const kvtc_requests* reque
  * over the tokens t < lens[i], or with a selection over those of them in the
  * selected pages (of a request with m pages the first min(budget, m) entries
  * are read; entries below 0 or past its pages are left out, a page listed
- * twice counts twice). out may take the place of q. No tokens: out = 0 and lse = -inf. Rows of
- * a page behind lens[i] are never used, whatever they hold. Sums and the
- * softmax's maximum and sum are fp32; out is rounded once. Equal calls give
- * equal bits. */
+ * twice counts twice). out may take the place of q. No tokens: out = 0 and
+ * lse = -inf. Rows of a page behind lens[i] are never used, whatever they hold.
+ * Sums and the softmax's maximum and sum are fp32; out is rounded once. Equal
+ * calls give equal bits. */
 kvtc_status kvtc_page_attend(const kvtc_pages* pages, const kvtc_requests* requests,
                              const kvtc_queries* queries, const kvtc_selection* selection,
                              void* d_ws, size_t ws_bytes, hipStream_t stream);
